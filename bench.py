@@ -881,8 +881,9 @@ def recorded_traffic(config: str, kernel: str, context_tokens: int):
 
 # sources off the 16-bit decode path whose traffic profiles/traffic.json
 # records: the chunked-prefill kernel, its tensor-core helpers, the
-# shared-prefix kernel and the fp8 page steps
-OFF_DECODE_PATH = ("pa_prefill.cuh", "pa_umma.cuh", "pa_shared_prefix.cuh", "pa_decode_fp8.cuh")
+# shared-prefix kernel, the fp8 page steps and the eviction kernels
+OFF_DECODE_PATH = ("pa_prefill.cuh", "pa_umma.cuh", "pa_shared_prefix.cuh", "pa_decode_fp8.cuh",
+                   "pa_evict.cuh")
 
 
 def kernel_source_digest(csrc: Path | None = None) -> str:

@@ -70,7 +70,9 @@ enum {
     PA_CHECK_WAIT_TIMEOUT = 5,  /* a shared-memory barrier wait gave up; index = CTA id */
     PA_CHECK_GROUP = 6,         /* malformed group bounds or prefix length; index = group */
     PA_CHECK_QUERY = 7,         /* prefill: q_len < 0, q_len > context_lens[s] or context too long; index = s */
-    PA_CHECK_VALUE = 8          /* prefill, bf16: a V value beyond the fp16 range was clamped to +-65504; index = s */
+    PA_CHECK_VALUE = 8,         /* prefill, bf16: a V value beyond the fp16 range was clamped to +-65504; index = s */
+    PA_CHECK_SOURCE = 9         /* evict: source[i] neither i nor a slot in [new_lens[s], context_lens[s]);
+                                   index = (s*num_kv_heads + kv)*budget + i */
 };
 
 /* Short English name of a status code (static string, never NULL). */
@@ -336,6 +338,69 @@ pa_status pa_prefill(void *out, const void *query, const void *key_cache,
                      int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
                      int64_t num_blocks, int64_t block_size, int64_t max_blocks_per_seq,
                      pa_dtype dtype, void *stream);
+
+/*
+ * Eviction from the paged cache by accumulated attention weight.  The pages
+ * have no counterpart: their caches only grow.  A sequence is held to `budget`
+ * tokens by keeping, for each KV head on its own, the first tokens (sinks),
+ * the latest ones, and of the others those that have received most attention.
+ * A token keeps the position its K row was written with; only its slot moves.
+ * The context length that the attention calls use afterwards is new_lens[s].
+ *   weights        [num_seqs, num_kv_heads, max_tokens] fp32: what the token in
+ *                  each slot has received (pa_prompt_weights, pa_decode_weights)
+ *   positions      [num_seqs, num_kv_heads, max_tokens] int32: position in its
+ *                  sequence of the token in each of the first recorded_lens[s]
+ *                  slots; the slots after them were filled in order, so that the
+ *                  one in slot i has position seq_lens[s] - context_lens[s] + i
+ *   context_lens   [num_seqs] int32: tokens in the cache, <= max_tokens
+ *   recorded_lens  [num_seqs] int32: 0 before the first eviction of a sequence,
+ *                  then the new_lens of the last one
+ *   seq_lens       [num_seqs] int32: tokens the sequence has had in all (equal
+ *                  to context_lens before its first eviction)
+ * max_tokens is at most 2^19 (PA_ERR_UNSUPPORTED beyond).
+ *
+ * pa_evict_select -- which tokens stay.
+ *   source    [num_seqs, num_kv_heads, budget] int32 (written)
+ *   new_lens  [num_seqs] int32 (written): min(context_lens[s], budget)
+ * Kept are the tokens at a position < sink or >= seq_lens[s] - recent
+ * (sink + recent <= budget), then the largest weights up to budget tokens; of
+ * equal weights those in the lowest slots (-0 equals +0, NaN counts below every
+ * number).  source[i], i < new_lens[s], is the slot whose token belongs in slot
+ * i: i itself if that token is kept, else the next kept token at or behind
+ * new_lens[s], in ascending order; source[i] = -1 from new_lens[s] on.  A
+ * sequence of at most budget tokens keeps all of them.  A context length outside
+ * [0, max_tokens] is reported (PA_CHECK_CONTEXT_LEN) and counts as 0.
+ */
+pa_status pa_evict_select(int32_t *source, int32_t *new_lens, const float *weights,
+                          const int32_t *positions, const int32_t *context_lens,
+                          const int32_t *recorded_lens, const int32_t *seq_lens,
+                          int64_t num_seqs, int64_t num_kv_heads, int64_t max_tokens,
+                          int64_t budget, int64_t sink, int64_t recent, void *stream);
+
+/*
+ * pa_evict_compact -- move what pa_evict_select kept: for every slot
+ * i < new_lens[s] of every KV head, the K and V rows, the weight and the
+ * position of slot source[i] go to slot i, and the first new_lens[s] positions
+ * are all recorded.  Slots from new_lens[s] on are left as they were; blocks
+ * that hold only such slots may be given back.  elem_bytes per cache element (2
+ * for fp16/bf16, 1 for fp8), block_size any positive value; a head's row must be
+ * a multiple of 16 bytes and both caches 16-byte aligned.  The sequence must own
+ * the blocks it writes: one shared with another sequence is copied first
+ * (pa_copy_blocks).  context_lens, recorded_lens and seq_lens as given to
+ * pa_evict_select; new_lens and source must not be written meanwhile.  Repeating
+ * the call changes nothing.  A source out of range (PA_CHECK_SOURCE) or a block id
+ * out of range (PA_CHECK_BLOCK_ID) is reported and its move left out; a
+ * sequence whose new_lens[s] is no length of its context is reported
+ * (PA_CHECK_CONTEXT_LEN) and left as it was.
+ */
+pa_status pa_evict_compact(void *key_cache, void *value_cache, float *weights,
+                           int32_t *positions, const int32_t *source, const int32_t *new_lens,
+                           const int32_t *block_tables, const int32_t *context_lens,
+                           const int32_t *recorded_lens, const int32_t *seq_lens,
+                           int64_t num_seqs, int64_t num_kv_heads, int64_t head_dim,
+                           int64_t num_blocks, int64_t block_size, int64_t max_blocks_per_seq,
+                           int64_t max_tokens, int64_t budget, int64_t elem_bytes,
+                           void *stream);
 
 /*
  * pa_check_error -- synchronise `stream`, read and clear the current device's

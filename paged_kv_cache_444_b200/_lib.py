@@ -24,7 +24,7 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_DTYP
                 4: "PA_ERR_ALIGN", 5: "PA_ERR_UNSUPPORTED", 6: "PA_ERR_CUDA",
                 7: "PA_ERR_BOUNDS"}
 CHECK_CODES = {1: "slot", 2: "block_id", 3: "context_len", 4: "partitions", 5: "wait_timeout",
-               6: "group", 7: "query", 8: "value"}
+               6: "group", 7: "query", 8: "value", 9: "source"}
 DTYPE_CODES = {torch.float16: 0, torch.bfloat16: 1}
 
 
@@ -71,6 +71,8 @@ SIGNATURES = {
     "pa_decode_step_host_workspace_bytes": (_i64, [_i64] * 7),
     "pa_decode_step_host": (_i, [_p] * 10 + [_i64, _f] + [_i64] * 8 + [_i, _p]),
     "pa_prefill": (_i, [_p] * 7 + [_f] + [_i64] * 9 + [_i, _p]),
+    "pa_evict_select": (_i, [_p] * 7 + [_i64] * 6 + [_p]),
+    "pa_evict_compact": (_i, [_p] * 10 + [_i64] * 9 + [_p]),
 }
 
 _lib: ctypes.CDLL | None = None
@@ -145,6 +147,16 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _need(cond: bool, msg: str) -> None:
     if not cond:
         raise ValueError(msg)
+
+
+def _on_one_device(stream, *tensors) -> None:
+    """The library launches on the current device: every tensor must be there
+    (and the stream, when it is a torch stream)."""
+    dev = tensors[0].device
+    _need(dev.type == "cuda" and all(t.device == dev for t in tensors),
+          "tensors must be on one CUDA device")
+    _need(dev.index == torch.cuda.current_device(), "tensors must be on the current device")
+    _need(getattr(stream, "device", dev) == dev, "stream and tensors must be on one device")
 
 
 # ---------------------------------------------------------------------------
@@ -369,6 +381,68 @@ def pa_prefill(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
                            int(max_query_len), H, Hk, D, NB, bs, block_tables.shape[1],
                            _dtype_code(query), _stream(stream))
     _check(st, "pa_prefill")
+
+
+def _evict_common(weights, positions, source, new_lens, context_lens, recorded_lens, seq_lens):
+    _need(weights.dtype == torch.float32 and weights.dim() == 3 and weights.is_contiguous(),
+          "weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
+    S, Hk, W = weights.shape
+    _need(positions.dtype == torch.int32 and positions.shape == weights.shape and
+          positions.is_contiguous(), "positions must be int32, shaped like weights")
+    _need(source.dtype == torch.int32 and source.dim() == 3 and source.shape[:2] == (S, Hk) and
+          source.is_contiguous(), "source must be [num_seqs, num_kv_heads, budget] int32")
+    for name, t in (("new_lens", new_lens), ("context_lens", context_lens),
+                    ("recorded_lens", recorded_lens), ("seq_lens", seq_lens)):
+        _need(t.dtype == torch.int32 and t.shape == (S,) and t.is_contiguous(),
+              f"{name} must be [num_seqs] int32")
+    _need(new_lens.data_ptr() not in (context_lens.data_ptr(), recorded_lens.data_ptr()) or S == 0,
+          "new_lens must not share storage with context_lens or recorded_lens")
+    return S, Hk, W, source.shape[2]
+
+
+def pa_evict_select(source: torch.Tensor, new_lens: torch.Tensor, weights: torch.Tensor,
+                    positions: torch.Tensor, context_lens: torch.Tensor,
+                    recorded_lens: torch.Tensor, seq_lens: torch.Tensor, sink: int, recent: int,
+                    stream=None) -> None:
+    """Which tokens of every (sequence, KV head) stay: source [S, Hk, budget]
+    int32 receives, for each slot of the packed cache, the slot its row comes
+    from; new_lens [S] int32 the packed lengths."""
+    S, Hk, W, B = _evict_common(weights, positions, source, new_lens, context_lens,
+                                recorded_lens, seq_lens)
+    _on_one_device(stream, weights, positions, source, new_lens, context_lens, recorded_lens,
+                   seq_lens)
+    st = load().pa_evict_select(source.data_ptr(), new_lens.data_ptr(), weights.data_ptr(),
+                                positions.data_ptr(), context_lens.data_ptr(),
+                                recorded_lens.data_ptr(), seq_lens.data_ptr(), S, Hk, W, B,
+                                int(sink), int(recent), _stream(stream))
+    _check(st, "pa_evict_select")
+
+
+def pa_evict_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, weights: torch.Tensor,
+                     positions: torch.Tensor, source: torch.Tensor, new_lens: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     recorded_lens: torch.Tensor, seq_lens: torch.Tensor, stream=None) -> None:
+    """Move the rows, weights and positions that pa_evict_select kept into the
+    first new_lens[s] slots; caches [NB, bs, Hk, D] contiguous, 16-bit or uint8."""
+    S, Hk, W, B = _evict_common(weights, positions, source, new_lens, context_lens,
+                                recorded_lens, seq_lens)
+    NB, bs, Hk2, D = key_cache.shape
+    _need(Hk2 == Hk, "caches and weights differ in num_kv_heads")
+    _need(value_cache.shape == key_cache.shape and key_cache.dtype == value_cache.dtype,
+          "key/value caches differ")
+    _need(key_cache.is_contiguous() and value_cache.is_contiguous(), "caches must be contiguous")
+    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and
+          block_tables.shape[0] == S and block_tables.is_contiguous(),
+          "block_tables must be [num_seqs, max_blocks] int32 contiguous")
+    _on_one_device(stream, key_cache, value_cache, weights, positions, source, new_lens,
+                   block_tables, context_lens, recorded_lens, seq_lens)
+    st = load().pa_evict_compact(key_cache.data_ptr(), value_cache.data_ptr(),
+                                 weights.data_ptr(), positions.data_ptr(), source.data_ptr(),
+                                 new_lens.data_ptr(), block_tables.data_ptr(),
+                                 context_lens.data_ptr(), recorded_lens.data_ptr(),
+                                 seq_lens.data_ptr(), S, Hk, D, NB, bs, block_tables.shape[1], W,
+                                 B, key_cache.element_size(), _stream(stream))
+    _check(st, "pa_evict_compact")
 
 
 class DecodePlan:

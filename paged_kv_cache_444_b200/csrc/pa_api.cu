@@ -1194,3 +1194,120 @@ extern "C" pa_status pa_prefill(void* out, const void* query, const void* key_ca
               : launch_prefill_t<128, false>(qm, km, vm, a, items, s);
 }
 // <<< chunked prefill
+
+// >>> eviction (pa_evict_select, pa_evict_compact): host side.
+#include "pa_evict.cuh"
+
+namespace {
+constexpr int64_t kSelectMaxTokens = 1 << 19;   // the list of moved slots fits eight CTAs
+constexpr int kSelectSmem = 227 * 1024;
+#ifndef PA_SELECT_RUN
+#define PA_SELECT_RUN 16384   // slots a CTA of a cluster takes
+#endif
+
+// The arguments both calls share (host only, no CUDA calls).
+pa_status check_evict_args(const void* source, const void* new_lens, const void* weights,
+                           const void* positions, const void* context_lens,
+                           const void* recorded_lens, const void* seq_lens, int64_t num_seqs,
+                           int64_t num_kv_heads, int64_t max_tokens, int64_t budget) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || max_tokens <= 0 || budget <= 0) return PA_ERR_SHAPE;
+  if (budget > INT32_MAX || num_seqs * num_kv_heads > INT32_MAX / 8) return PA_ERR_SHAPE;
+  if (max_tokens > kSelectMaxTokens) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  const void* all[] = {source,       new_lens,      weights, positions,
+                       context_lens, recorded_lens, seq_lens};
+  for (const void* p : all)
+    if (!p) return PA_ERR_NULL;
+  for (const void* p : all)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return PA_ERR_ALIGN;
+  return PA_OK;
+}
+}  // namespace
+
+extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const float* weights,
+                                     const int32_t* positions, const int32_t* context_lens,
+                                     const int32_t* recorded_lens, const int32_t* seq_lens,
+                                     int64_t num_seqs, int64_t num_kv_heads, int64_t max_tokens,
+                                     int64_t budget, int64_t sink, int64_t recent, void* stream) {
+  const pa_status st = check_evict_args(source, new_lens, weights, positions, context_lens,
+                                        recorded_lens, seq_lens, num_seqs, num_kv_heads,
+                                        max_tokens, budget);
+  if (st != PA_OK) return st;
+  if (sink < 0 || recent < 0 || sink > budget || recent > budget - sink) return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  EvictArgs a{};
+  a.source = source;
+  a.new_lens = new_lens;
+  a.weights = const_cast<float*>(weights);
+  a.positions = const_cast<int32_t*>(positions);
+  a.context_lens = context_lens;
+  a.recorded_lens = recorded_lens;
+  a.seq_lens = seq_lens;
+  a.num_kv_heads = static_cast<int>(num_kv_heads);
+  a.max_tokens = static_cast<int>(max_tokens);
+  a.budget = static_cast<int>(budget);
+  a.sink = static_cast<int>(sink);
+  a.recent = static_cast<int>(recent);
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(evict_select_kernel, kSelectSmem, &done)) return PA_ERR_CUDA;
+  int c = 1;
+  while (c < 8 && static_cast<int64_t>(c) * PA_SELECT_RUN < max_tokens) c *= 2;
+  const int run = (static_cast<int>((max_tokens + c - 1) / c) + 31) & ~31;
+  const int64_t most = budget < max_tokens / 2 ? budget : max_tokens / 2;
+  const int list = static_cast<int>((most + c - 1) / c) + 1;
+  const int cached = select_smem(run, true, list) <= kSelectSmem;
+  return launch_ex(evict_select_kernel, static_cast<unsigned>(num_seqs * num_kv_heads * c),
+                   kSelectThreads, select_smem(run, cached != 0, list), as_stream(stream), c, a,
+                   run, cached);
+}
+
+extern "C" pa_status pa_evict_compact(void* key_cache, void* value_cache, float* weights,
+                                      int32_t* positions, const int32_t* source,
+                                      const int32_t* new_lens, const int32_t* block_tables,
+                                      const int32_t* context_lens, const int32_t* recorded_lens,
+                                      const int32_t* seq_lens, int64_t num_seqs,
+                                      int64_t num_kv_heads, int64_t head_dim, int64_t num_blocks,
+                                      int64_t block_size, int64_t max_blocks_per_seq,
+                                      int64_t max_tokens, int64_t budget, int64_t elem_bytes,
+                                      void* stream) {
+  const pa_status st = check_evict_args(source, new_lens, weights, positions, context_lens,
+                                        recorded_lens, seq_lens, num_seqs, num_kv_heads,
+                                        max_tokens, budget);
+  if (st != PA_OK) return st;
+  if (head_dim <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks_per_seq <= 0)
+    return PA_ERR_SHAPE;
+  if (elem_bytes != 1 && elem_bytes != 2) return PA_ERR_SHAPE;
+  if (head_dim > INT32_MAX / 2 || num_blocks > INT32_MAX / block_size ||
+      max_blocks_per_seq > INT32_MAX / block_size)
+    return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (!key_cache || !value_cache || !block_tables) return PA_ERR_NULL;
+  if (head_dim * elem_bytes % 16 != 0 || !aligned16(key_cache) || !aligned16(value_cache) ||
+      (reinterpret_cast<uintptr_t>(block_tables) & 3u))
+    return PA_ERR_ALIGN;
+  CompactArgs a{};
+  a.e.source = const_cast<int32_t*>(source);
+  a.e.new_lens = const_cast<int32_t*>(new_lens);
+  a.e.weights = weights;
+  a.e.positions = positions;
+  a.e.context_lens = context_lens;
+  a.e.recorded_lens = recorded_lens;
+  a.e.seq_lens = seq_lens;
+  a.e.num_kv_heads = static_cast<int>(num_kv_heads);
+  a.e.max_tokens = static_cast<int>(max_tokens);
+  a.e.budget = static_cast<int>(budget);
+  a.key_cache = static_cast<uint8_t*>(key_cache);
+  a.value_cache = static_cast<uint8_t*>(value_cache);
+  a.block_tables = block_tables;
+  a.block_size = static_cast<int>(block_size);
+  a.num_blocks = static_cast<int>(num_blocks);
+  a.max_blocks_per_seq = static_cast<int>(max_blocks_per_seq);
+  a.row_units = static_cast<int>(head_dim * elem_bytes / 16);
+  const int64_t slots = budget < max_tokens ? budget : max_tokens;
+  a.chunks = static_cast<int>((slots + kCompactSlots - 1) / kCompactSlots);
+  const int64_t grid = num_seqs * num_kv_heads * a.chunks;
+  if (grid > INT32_MAX) return PA_ERR_SHAPE;
+  return launch_ex(evict_compact_kernel, static_cast<unsigned>(grid), kCompactThreads, 0,
+                   as_stream(stream), 1, a);
+}
+// <<< eviction

@@ -1,0 +1,76 @@
+"""Refusals of the eviction calls, on the host (CPU only)."""
+import pytest
+import torch
+
+from paged_kv_cache_444_b200 import _lib, pa_evict_compact, pa_evict_select
+
+OK, NULL, SHAPE, DTYPE, ALIGN, UNSUP, CUDA, BOUNDS = range(8)
+FAKE = 0x10000
+
+host_only = pytest.mark.skipif(torch.cuda.is_available(),
+                               reason="stand-in pointers: host-only validation test")
+
+
+def _call(name, order, base, **kw):
+    args = dict(base)
+    assert set(kw) <= set(args)
+    args.update(kw)
+    return getattr(_lib.load(), name)(*(args[k] for k in order), None)
+
+
+SELECT_ORDER = ("source new_lens weights positions ctx recorded seq S Hk W B sink recent").split()
+SELECT_BASE = dict({k: FAKE for k in SELECT_ORDER[:7]}, S=4, Hk=2, W=100, B=32, sink=4, recent=8)
+COMPACT_ORDER = ("kc vc weights positions source new_lens bt ctx recorded seq S Hk D NB bs MB W B "
+                 "eb").split()
+COMPACT_BASE = dict({k: FAKE for k in COMPACT_ORDER[:10]}, S=4, Hk=2, D=128, NB=64, bs=16, MB=8,
+                    W=100, B=32, eb=2)
+
+
+@host_only
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(S=-1)), (SHAPE, dict(Hk=0)), (SHAPE, dict(W=0)), (SHAPE, dict(B=0)),
+    (SHAPE, dict(sink=-1)), (SHAPE, dict(recent=-1)), (SHAPE, dict(sink=25)),
+    (SHAPE, dict(sink=33, recent=0)), (SHAPE, dict(S=1 << 28, Hk=2)),
+    (UNSUP, dict(W=(1 << 19) + 1)), (NULL, dict(weights=None)), (NULL, dict(seq=None)),
+    (ALIGN, dict(source=FAKE + 2)), (OK, dict(S=0, source=None)), (CUDA, dict()),
+    (CUDA, dict(sink=24)),
+])
+def test_select_refusals(want, kw):
+    assert _call("pa_evict_select", SELECT_ORDER, SELECT_BASE, **kw) == want
+
+
+@host_only
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(S=-1)), (SHAPE, dict(D=0)), (SHAPE, dict(eb=4)), (SHAPE, dict(bs=0)),
+    (SHAPE, dict(NB=1 << 28)), (SHAPE, dict(MB=1 << 28)), (SHAPE, dict(B=1 << 31)),
+    (UNSUP, dict(W=(1 << 19) + 1)), (NULL, dict(kc=None)), (NULL, dict(bt=None)),
+    (NULL, dict(new_lens=None)), (ALIGN, dict(D=4)), (ALIGN, dict(D=8, eb=1)),
+    (ALIGN, dict(vc=FAKE + 8)), (ALIGN, dict(bt=FAKE + 2)), (ALIGN, dict(positions=FAKE + 1)),
+    (OK, dict(S=0)), (CUDA, dict()),
+])
+def test_compact_refusals(want, kw):
+    assert _call("pa_evict_compact", COMPACT_ORDER, COMPACT_BASE, **kw) == want
+
+
+def test_binding_refuses_wrong_tensors():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    good = dict(source=i32(2, 3, 8), new_lens=i32(2), weights=torch.zeros(2, 3, 20),
+                positions=i32(2, 3, 20), context_lens=i32(2), recorded_lens=i32(2),
+                seq_lens=i32(2))
+    lens = good["context_lens"]
+    for bad in (dict(weights=torch.zeros(2, 3, 20).half()), dict(weights=torch.zeros(3, 20)),
+                dict(weights=torch.zeros(2, 20, 3).transpose(1, 2)), dict(positions=i32(2, 3, 19)),
+                dict(source=i32(2, 2, 8)), dict(source=torch.zeros(2, 3, 8, dtype=torch.int64)),
+                dict(new_lens=i32(3)), dict(seq_lens=torch.zeros(2, dtype=torch.int64)),
+                dict(new_lens=lens),                 # in place: other heads still read it
+                {}):                                 # host tensors
+        with pytest.raises(ValueError):
+            pa_evict_select(**{**good, **bad}, sink=1, recent=2)
+    kc = torch.zeros(4, 16, 3, 64, dtype=torch.float16)
+    more = dict(key_cache=kc, value_cache=kc.clone(), block_tables=i32(2, 2))
+    for bad in (dict(value_cache=torch.zeros(4, 16, 3, 32, dtype=torch.float16)),
+                dict(key_cache=torch.zeros(4, 16, 2, 64, dtype=torch.float16)),
+                dict(value_cache=kc.bfloat16()), dict(block_tables=i32(3, 2)),
+                dict(block_tables=i32(2, 4)[:, ::2]), {}):
+        with pytest.raises(ValueError):
+            pa_evict_compact(**{**good, **more, **bad})

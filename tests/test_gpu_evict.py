@@ -1,0 +1,274 @@
+"""pa_evict_select and pa_evict_compact against a plain restatement on the host:
+whole numbers and moved bits, so every comparison is for equality."""
+import numpy as np
+import pytest
+import torch
+
+import evict_reference as ref
+from paged_kv_cache_444_b200 import (PagedAttentionError, pa_check_error, pa_evict_compact,
+                                     pa_evict_select)
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x, dev):
+    return torch.as_tensor(np.asarray(x, dtype=np.int32), device=dev)
+
+
+class Batch:
+    """Random weights and positions of a batch; `recorded` slots a sequence
+    were placed by an earlier eviction, the others follow in order."""
+
+    def __init__(self, dev, ctx, Hk, budget, seed, recorded=None, W=None, weights=None, age=7):
+        rng = np.random.default_rng(seed)
+        S = len(ctx)
+        self.W = W or max(max(ctx), 1)
+        self.budget, self.Hk, self.dev = budget, Hk, dev
+        self.ctx = np.array(ctx, dtype=np.int32)
+        self.recorded = np.array(recorded if recorded is not None else [0] * S, dtype=np.int32)
+        self.length = np.where(self.recorded > 0, self.ctx * age, self.ctx).astype(np.int32)
+        self.weights = (np.exp(2 * rng.standard_normal((S, Hk, self.W))).astype(np.float32)
+                        if weights is None else weights(rng, (S, Hk, self.W)))
+        self.positions = rng.integers(-9, 9, (S, Hk, self.W)).astype(np.int32)  # unread garbage
+        for s in range(S):
+            r = int(self.recorded[s])
+            for h in range(Hk):
+                first = int(self.length[s]) - (int(self.ctx[s]) - r)
+                self.positions[s, h, :r] = rng.permutation(first)[:r]
+        self.t = {k: torch.as_tensor(getattr(self, k), device=dev) for k in
+                  ("weights", "positions", "ctx", "recorded", "length")}
+        self.source = torch.full((S, Hk, budget), -7, dtype=torch.int32, device=dev)
+        self.new_lens = torch.full((S,), -7, dtype=torch.int32, device=dev)
+
+    def select(self, sink, recent, stream=None):
+        pa_evict_select(self.source, self.new_lens, self.t["weights"], self.t["positions"],
+                        self.t["ctx"], self.t["recorded"], self.t["length"], sink, recent, stream)
+
+    def want(self, sink, recent):
+        return ref.select(self.weights, self.positions, self.recorded, self.length, self.ctx,
+                          self.budget, sink, recent)
+
+    def check_select(self, sink, recent):
+        self.select(sink, recent)
+        torch.cuda.synchronize()
+        pa_check_error()
+        source, new = self.want(sink, recent)
+        assert np.array_equal(self.new_lens.cpu().numpy(), new)
+        got = self.source.cpu().numpy()
+        bad = np.argwhere(got != source)
+        assert bad.size == 0, (bad[:4], got[tuple(bad[0])], source[tuple(bad[0])])
+
+
+def _ties(rng, shape):       # few values, both zeros among them
+    return rng.choice(np.array([0.0, -0.0, 0.25, 0.5], dtype=np.float32), shape)
+
+
+def _equal(rng, shape):
+    return np.full(shape, 0.125, dtype=np.float32)
+
+
+def _odd(rng, shape):        # NaN, infinities, denormals, negatives
+    w = rng.standard_normal(shape).astype(np.float32)
+    pick = rng.integers(0, 8, shape)
+    w[pick == 0] = np.nan
+    w[pick == 1] = np.inf
+    w[pick == 2] = -np.inf
+    w[pick == 3] = 1e-42
+    return w
+
+
+SELECT = {
+    # name: (contexts, KV heads, budget, sink, recent, options)
+    "one_token": ((1,), 1, 1, 0, 0, {}),
+    "two_of_three": ((3,), 2, 2, 1, 1, {}),
+    "empty_and_short": ((0, 1, 5, 6, 7), 3, 6, 1, 2, {}),
+    "one_over": ((33, 34, 65), 2, 32, 4, 8, {}),
+    "all_held": ((40, 50), 2, 32, 12, 20, {}),
+    "nothing_held": ((1000, 31, 999), 2, 100, 0, 0, {}),
+    "odd_width": ((777, 1025, 1024), 3, 333, 4, 50, dict(W=1111)),
+    "steady": ((130, 147, 129), 4, 128, 4, 30, dict(recorded=(128, 128, 128))),
+    "steady_mixed": ((130, 100, 300), 2, 128, 2, 16, dict(recorded=(128, 0, 128))),
+    "budget_over_width": ((50, 60), 2, 100, 4, 8, {}),
+    "ties": ((500, 2000), 2, 200, 3, 10, dict(weights=_ties)),
+    "equal": ((700, 1300), 2, 512, 0, 5, dict(weights=_equal)),
+    "odd_values": ((900, 1500), 2, 300, 4, 10, dict(weights=_odd)),
+    "mostly_nan": ((400,), 1, 390, 0, 0, dict(weights=_odd)),
+    "long": ((20000, 16384, 9), 2, 3000, 4, 100, {}),
+    "cluster_ties": ((40000,), 2, 25000, 4, 100, dict(weights=_ties)),
+    "cluster_of_eight": ((131072, 70001), 1, 4096, 4, 512, {}),
+    "cluster_equal": ((100001,), 1, 60000, 1, 7, dict(weights=_equal)),
+    "wide_table": ((300, 200), 2, 100, 4, 10, dict(W=524288)),
+}
+
+
+@pytest.mark.parametrize("name", SELECT)
+def test_select_matches_the_plain_form(name, cuda_device):
+    ctx, Hk, budget, sink, recent, kw = SELECT[name]
+    Batch(cuda_device, ctx, Hk, budget, 500 + len(name), **kw).check_select(sink, recent)
+
+
+def test_select_where_keys_do_not_fit_shared_memory(cuda_device):
+    """The longest context the call takes: a CTA's run of 65536 slots is read
+    again for every digit.  numpy's stable sort stands in for the slow loop."""
+    n, B, sink, recent = 524288, 200000, 4, 1000
+    b = Batch(cuda_device, (n,), 1, B, 91)
+    b.select(sink, recent)
+    torch.cuda.synchronize()
+    pa_check_error()
+    w = b.weights[0, 0].astype(np.float64)
+    w[:sink] = np.inf
+    w[n - recent:] = np.inf
+    kept = np.zeros(n, bool)
+    kept[np.argsort(-w, kind="stable")[:B]] = True
+    want = np.arange(B)
+    want[~kept[:B]] = B + np.flatnonzero(kept[B:])
+    assert np.array_equal(b.source[0, 0].cpu().numpy(), want)
+
+
+def test_select_reports_a_bad_context_length(cuda_device):
+    b = Batch(cuda_device, (50, 60, 20), 2, 16, 92)
+    b.t["ctx"] = _i32([50, 61, 20], cuda_device)      # past max_tokens
+    b.select(1, 4)
+    with pytest.raises(PagedAttentionError, match="context_len, index 1"):
+        pa_check_error()
+    pa_check_error()                                  # cleared
+    source, new = b.want(1, 4)
+    assert np.array_equal(b.new_lens.cpu().numpy(), [16, 0, 16])
+    got = b.source.cpu().numpy()
+    assert np.array_equal(got[[0, 2]], source[[0, 2]]) and (got[1] == -1).all()
+
+
+def _caches(dev, b, D, dtype, bs, seed, spare=3):
+    """Caches of random bits and tables of distinct blocks, -1 past each end."""
+    rng = np.random.default_rng(seed)
+    need = [-(-int(c) // bs) for c in b.ctx]
+    width = max(1, *need)
+    perm = rng.permutation(sum(need) + spare).astype(np.int32)
+    tables, at = np.full((len(need), width), -1, dtype=np.int32), 0
+    for s, m in enumerate(need):
+        tables[s, :m] = perm[at:at + m]
+        at += m
+    kind = np.uint8 if dtype == torch.uint8 else np.uint16
+    shape = (sum(need) + spare, bs, b.Hk, D)
+    kc, vc = (rng.integers(0, np.iinfo(kind).max, shape, endpoint=True).astype(kind)
+              for _ in range(2))
+    to = lambda x: torch.as_tensor(x.view(np.int16) if kind == np.uint16 else x,
+                                   device=dev).view(dtype)
+    return kc, vc, tables, to(kc), to(vc)
+
+
+def _bits(t):
+    t = t.cpu()
+    return t.numpy() if t.dtype == torch.uint8 else t.view(torch.int16).numpy().view(np.uint16)
+
+
+COMPACT = {
+    # name: (select case, head_dim, dtype, block size)
+    "tiny_f16": ("two_of_three", 64, torch.float16, 16),
+    "empty_bf16": ("empty_and_short", 128, torch.bfloat16, 16),
+    "one_over_fp8": ("one_over", 128, torch.uint8, 16),
+    "nothing_held_bf16": ("nothing_held", 128, torch.bfloat16, 16),
+    "odd_width_d8": ("odd_width", 8, torch.float16, 16),
+    "steady_bf16": ("steady", 128, torch.bfloat16, 16),
+    "steady_mixed_f16": ("steady_mixed", 64, torch.float16, 16),
+    "budget_over_width": ("budget_over_width", 128, torch.bfloat16, 16),
+    "block_of_five": ("one_over", 16, torch.uint8, 5),
+    "long_bf16": ("long", 64, torch.bfloat16, 16),
+}
+
+
+@pytest.mark.parametrize("name", COMPACT)
+def test_compact_moves_what_select_kept(name, cuda_device):
+    case, D, dtype, bs = COMPACT[name]
+    ctx, Hk, budget, sink, recent, kw = SELECT[case]
+    b = Batch(cuda_device, ctx, Hk, budget, 700 + len(name), **kw)
+    kc, vc, tables, kd, vd = _caches(cuda_device, b, D, dtype, bs, 701)
+    b.select(sink, recent)
+    source, new = b.want(sink, recent)
+    want = ref.compact(kc, vc, b.weights, b.positions, source, new, tables, b.ctx, b.recorded,
+                       b.length)
+    td = torch.as_tensor(tables, device=cuda_device)
+    for again in range(2):     # repeating the call changes nothing
+        pa_evict_compact(kd, vd, b.t["weights"], b.t["positions"], b.source, b.new_lens, td,
+                         b.t["ctx"], b.t["recorded"], b.t["length"])
+        torch.cuda.synchronize()
+        pa_check_error()
+        assert np.array_equal(_bits(kd), want[0]) and np.array_equal(_bits(vd), want[1])
+        assert np.array_equal(b.t["weights"].cpu().numpy(), want[2])
+        assert np.array_equal(b.t["positions"].cpu().numpy(), want[3])
+
+
+def test_compact_leaves_out_bad_sources_and_blocks(cuda_device):
+    """A source out of range and a block id out of range are reported, their
+    moves left out; a new length that cannot be is reported, its sequence left."""
+    b = Batch(cuda_device, (40, 40, 40), 1, 20, 93, weights=_equal)
+    kc, vc, tables, kd, vd = _caches(cuda_device, b, 64, torch.float16, 16, 94)
+    b.select(0, 5)                                   # slots 15..19 <- 35..39
+    source, new = b.want(0, 5)
+    assert (source[0, 0, 15:] == np.arange(35, 40)).all()
+
+    def run(src, lens, tab):
+        w, p = b.t["weights"].clone(), b.t["positions"].clone()
+        k, v = kd.clone(), vd.clone()
+        pa_evict_compact(k, v, w, p, _i32(src, cuda_device), _i32(lens, cuda_device),
+                         torch.as_tensor(tab, device=cuda_device), b.t["ctx"], b.t["recorded"],
+                         b.t["length"])
+        return k, v
+
+    bad = source.copy()
+    bad[1, 0, 17] = 40                               # at the context's end
+    good = source.copy()
+    good[1, 0, 17] = 17
+    k, v = run(bad, new, tables)
+    with pytest.raises(PagedAttentionError, match="source, index 37"):
+        pa_check_error()
+    want = ref.compact(kc, vc, b.weights, b.positions, good, new, tables, b.ctx, b.recorded,
+                       b.length)
+    assert np.array_equal(_bits(k), want[0]) and np.array_equal(_bits(v), want[1])
+
+    bad[1, 0, 17] = 3                                # below the new length, not itself
+    k, _ = run(bad, new, tables)
+    with pytest.raises(PagedAttentionError, match="source, index 37"):
+        pa_check_error()
+    assert np.array_equal(_bits(k), want[0])
+
+    broken = tables.copy()
+    broken[2, 2] = kc.shape[0]                       # slots 32.. of sequence 2
+    stay = source.copy()
+    stay[2, 0, 15:] = np.arange(15, 20)
+    k, v = run(source, new, broken)
+    with pytest.raises(PagedAttentionError, match="block_id, index 8"):
+        pa_check_error()
+    want = ref.compact(kc, vc, b.weights, b.positions, stay, new, tables, b.ctx, b.recorded,
+                       b.length)
+    assert np.array_equal(_bits(k), want[0]) and np.array_equal(_bits(v), want[1])
+
+    k, v = run(source, [20, 21, 20], tables)         # more than the budget
+    with pytest.raises(PagedAttentionError, match="context_len, index 1"):
+        pa_check_error()
+    stay = source.copy()
+    stay[1, 0, 15:] = np.arange(15, 20)
+    want = ref.compact(kc, vc, b.weights, b.positions, stay, new, tables, b.ctx, b.recorded,
+                       b.length)
+    assert np.array_equal(_bits(k), want[0])
+    pa_check_error()
+
+
+def test_select_on_another_stream_and_in_a_graph(cuda_device):
+    """The call goes to the stream it is given, and replays read the buffers' new contents."""
+    b = Batch(cuda_device, (600, 90), 2, 64, 95)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    b.select(2, 8, stream=other)
+    other.synchronize()
+    assert np.array_equal(b.source.cpu().numpy(), b.want(2, 8)[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.select(2, 8)
+    for seed in (1, 2):
+        b.weights = np.random.default_rng(seed).random(b.weights.shape, dtype=np.float32)
+        b.t["weights"].copy_(torch.as_tensor(b.weights))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(b.source.cpu().numpy(), b.want(2, 8)[0])
+    pa_check_error()
