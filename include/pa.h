@@ -340,6 +340,34 @@ pa_status pa_prefill(void *out, const void *query, const void *key_cache,
                      pa_dtype dtype, void *stream);
 
 /*
+ * pa_decode_weights -- pa_decode that also adds up what each cached token
+ * receives, the score that pa_evict_select keeps tokens by.
+ *   weights    [num_seqs, num_kv_heads, max_tokens] fp32 (updated): for every
+ *              token j < context_lens[s] of KV head kv, the sum over the query
+ *              heads h of kv of softmax_j(scale * q[s,h,:] . k_j)
+ *   new_tokens the last new_tokens tokens of each context are new: their
+ *              entries are set to that sum, the earlier ones have it added.
+ *              (1 in a decode step; entries behind the context stay as they are,
+ *              so nothing needs clearing.)
+ *   workspace  caller-owned device memory, 256-byte aligned, of at least
+ *              pa_decode_weights_workspace_bytes(...) bytes; holds nothing
+ *              between calls, and calls that may overlap need one each
+ * Other arguments, layouts and limits as pa_decode.  A context longer than
+ * max_tokens is reported (PA_CHECK_CONTEXT_LEN): its output is computed, its
+ * weights stay as they were.
+ */
+int64_t pa_decode_weights_workspace_bytes(int64_t num_seqs, int64_t num_heads, int64_t head_dim,
+                                          int64_t max_blocks_per_seq, int64_t block_size);
+
+pa_status pa_decode_weights(void *out, float *weights, void *workspace, int64_t workspace_bytes,
+                            const void *query, const void *key_cache, const void *value_cache,
+                            const int32_t *block_tables, const int32_t *context_lens,
+                            float scale, int64_t num_seqs, int64_t num_heads,
+                            int64_t num_kv_heads, int64_t head_dim, int64_t num_blocks,
+                            int64_t block_size, int64_t max_blocks_per_seq, int64_t max_tokens,
+                            int64_t new_tokens, pa_dtype dtype, void *stream);
+
+/*
  * Eviction from the paged cache by accumulated attention weight.  The pages
  * have no counterpart: their caches only grow.  A sequence is held to `budget`
  * tokens by keeping, for each KV head on its own, the first tokens (sinks),

@@ -12,15 +12,15 @@ import torch
 
 from ._lib import (DecodePlan, HostStep, PagedAttentionError, load, pa_check_error, pa_copy_blocks, pa_decode,
                    pa_decode_fp8, pa_decode_noalloc, pa_decode_shared_prefix, pa_decode_split,
-                   pa_decode_split_fp8, pa_evict_compact, pa_evict_select, pa_prefill, pa_reduce,
-                   pa_reshape_and_cache, pa_reshape_and_cache_fp8, pa_selftest_wait_timeout)
+                   pa_decode_split_fp8, pa_decode_weights, pa_evict_compact, pa_evict_select,
+                   pa_prefill, pa_reduce, pa_reshape_and_cache, pa_reshape_and_cache_fp8, pa_selftest_wait_timeout)
 
 __all__ = [
     "PagedAttentionError", "load", "pa_reshape_and_cache", "pa_decode", "pa_decode_split",
     "pa_reduce", "pa_check_error", "pa_decode_noalloc", "pa_decode_shared_prefix",
     "pa_copy_blocks", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_split_fp8",
-    "pa_prefill", "pa_evict_select", "pa_evict_compact", "pa_selftest_wait_timeout",
-    "SplitWorkspace", "decode_step", "HostStep", "DecodePlan",
+    "pa_prefill", "pa_decode_weights", "pa_evict_select", "pa_evict_compact", "pa_selftest_wait_timeout",
+    "SplitWorkspace", "WeightsWorkspace", "decode_step", "HostStep", "DecodePlan",
 ]
 
 
@@ -38,6 +38,26 @@ class SplitWorkspace:
     @property
     def max_partitions(self) -> int:
         return self.max_logits.shape[-1]
+
+
+class WeightsWorkspace:
+    """Caller-owned scratch for pa_decode_weights (one for calls that follow one
+    another; calls that may overlap on the GPU need one each)."""
+
+    def __init__(self, num_seqs: int, num_heads: int, head_dim: int, max_blocks_per_seq: int,
+                 device: torch.device | str, block_size: int = 16):
+        n = load().pa_decode_weights_workspace_bytes(num_seqs, num_heads, head_dim,
+                                                     max_blocks_per_seq, block_size)
+        if n < 0:
+            raise ValueError("bad workspace sizes")
+        self.buffer = torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+    @classmethod
+    def for_call(cls, query: torch.Tensor, key_cache: torch.Tensor,
+                 block_tables: torch.Tensor) -> "WeightsWorkspace":
+        """The workspace of a call with these tensors."""
+        S, H, D = query.shape
+        return cls(S, H, D, block_tables.shape[1], query.device, key_cache.shape[1])
 
 
 def decode_step(query, key, value, key_cache, value_cache, slot_mapping, block_tables,

@@ -71,6 +71,8 @@ SIGNATURES = {
     "pa_decode_step_host_workspace_bytes": (_i64, [_i64] * 7),
     "pa_decode_step_host": (_i, [_p] * 10 + [_i64, _f] + [_i64] * 8 + [_i, _p]),
     "pa_prefill": (_i, [_p] * 7 + [_f] + [_i64] * 9 + [_i, _p]),
+    "pa_decode_weights_workspace_bytes": (_i64, [_i64] * 5),
+    "pa_decode_weights": (_i, [_p] * 3 + [_i64] + [_p] * 5 + [_f] + [_i64] * 9 + [_i, _p]),
     "pa_evict_select": (_i, [_p] * 7 + [_i64] * 6 + [_p]),
     "pa_evict_compact": (_i, [_p] * 10 + [_i64] * 9 + [_p]),
 }
@@ -381,6 +383,32 @@ def pa_prefill(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
                            int(max_query_len), H, Hk, D, NB, bs, block_tables.shape[1],
                            _dtype_code(query), _stream(stream))
     _check(st, "pa_prefill")
+
+
+def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, workspace, query: torch.Tensor,
+                      key_cache: torch.Tensor, value_cache: torch.Tensor,
+                      block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                      new_tokens: int = 1, stream=None) -> None:
+    """pa_decode that adds the attention weight each cached token receives to
+    weights [S, Hk, max_tokens] float32 (and sets it for the last new_tokens
+    tokens of each context); workspace: a WeightsWorkspace for these sizes."""
+    S, H, D, NB, bs, Hk, MB, dt = _attention_common(query, key_cache, value_cache,
+                                                    block_tables, context_lens)
+    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
+          "out must match query")
+    _need(weights.dtype == torch.float32 and weights.dim() == 3 and
+          weights.shape[:2] == (S, Hk) and weights.is_contiguous(),
+          "weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
+    _need(context_lens.is_contiguous(), "context_lens must be contiguous")
+    buf = workspace.buffer
+    _on_one_device(stream, query, out, weights, buf, key_cache, value_cache, block_tables,
+                   context_lens)
+    st = load().pa_decode_weights(out.data_ptr(), weights.data_ptr(), buf.data_ptr(), buf.numel(),
+                                  query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                  block_tables.data_ptr(), context_lens.data_ptr(), float(scale),
+                                  S, H, Hk, D, NB, bs, MB, weights.shape[2], int(new_tokens), dt,
+                                  _stream(stream))
+    _check(st, "pa_decode_weights")
 
 
 def _evict_common(weights, positions, source, new_lens, context_lens, recorded_lens, seq_lens):

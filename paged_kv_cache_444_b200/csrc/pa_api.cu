@@ -1311,3 +1311,121 @@ extern "C" pa_status pa_evict_compact(void* key_cache, void* value_cache, float*
                    as_stream(stream), 1, a);
 }
 // <<< eviction
+
+// >>> decode that adds up attention weights (pa_decode_weights): host side.
+#include "pa_decode_weights.cuh"
+
+namespace {
+// Workspace parts, each 256-byte aligned: tmp_out, part_m, part_l, logits.
+struct WeightsLayout {
+  int64_t off[4];
+  int64_t total, parts;
+};
+
+WeightsLayout weights_layout(int64_t S, int64_t H, int64_t D, int64_t MB, int64_t bs) {
+  WeightsLayout l{};
+  l.parts = (MB * bs + kWeightsPart - 1) / kWeightsPart;
+  const int64_t rows = S * H * l.parts;
+  const int64_t sizes[4] = {rows * D * 4, rows * 4, rows * 4, S * H * MB * bs * 4};
+  for (int i = 0; i < 4; ++i) {
+    l.off[i] = l.total;
+    l.total = align256(l.total + sizes[i]);
+  }
+  return l;
+}
+
+template <int D, bool BF16, int NT>
+pa_status launch_weights_t(const CUtensorMap& km, const CUtensorMap& vm, const WeightsArgs& a,
+                           long long items, long long merge, cudaStream_t stream) {
+  constexpr int NST = Stages<D>::value;
+  using L = DecodeSmem<D, NST>;
+  auto kernel = weights_split_kernel<D, NST, BF16, NT>;
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(kernel, L::kAlloc, &done)) return PA_ERR_CUDA;
+  const pa_status st = launch_ex(kernel, static_cast<unsigned>(items), kThreads, L::kAlloc, stream,
+                                 1, km, vm, a);
+  if (st != PA_OK) return st;
+  return launch_ex(weights_merge_kernel<D, BF16>, static_cast<unsigned>(merge), kWeightsThreads, 0,
+                   stream, 1, a);
+}
+}  // namespace
+
+extern "C" int64_t pa_decode_weights_workspace_bytes(int64_t num_seqs, int64_t num_heads,
+                                                     int64_t head_dim,
+                                                     int64_t max_blocks_per_seq,
+                                                     int64_t block_size) {
+  if (num_seqs < 0 || num_heads <= 0 || head_dim <= 0 || max_blocks_per_seq <= 0 ||
+      block_size <= 0)
+    return -1;
+  return weights_layout(num_seqs, num_heads, head_dim, max_blocks_per_seq, block_size).total;
+}
+
+extern "C" pa_status pa_decode_weights(void* out, float* weights, void* workspace,
+                                       int64_t workspace_bytes, const void* query,
+                                       const void* key_cache, const void* value_cache,
+                                       const int32_t* block_tables, const int32_t* context_lens,
+                                       float scale, int64_t num_seqs, int64_t num_heads,
+                                       int64_t num_kv_heads, int64_t head_dim, int64_t num_blocks,
+                                       int64_t block_size, int64_t max_blocks_per_seq,
+                                       int64_t max_tokens, int64_t new_tokens, pa_dtype dtype,
+                                       void* stream) {
+  pa_status st = check_attention_args(query, key_cache, value_cache, block_tables, context_lens,
+                                      scale, num_seqs, num_heads, num_kv_heads, head_dim,
+                                      num_blocks, block_size, max_blocks_per_seq, dtype);
+  if (st != PA_OK) return st;
+  if (max_tokens <= 0 || max_tokens > INT32_MAX || new_tokens < 0 || new_tokens > INT32_MAX)
+    return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !weights || !workspace) return PA_ERR_NULL;
+  if (!aligned16(out) || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PA_ERR_ALIGN;
+  const WeightsLayout l =
+      weights_layout(num_seqs, num_heads, head_dim, max_blocks_per_seq, block_size);
+  if (workspace_bytes < l.total) return PA_ERR_SHAPE;
+  const int64_t runs = (max_blocks_per_seq * block_size + kWeightsRun - 1) / kWeightsRun;
+  const int64_t items = num_seqs * num_kv_heads * l.parts;
+  const int64_t merge = num_seqs * num_heads + num_seqs * num_kv_heads * runs;
+  if (items > INT32_MAX || merge > INT32_MAX) return PA_ERR_SHAPE;
+  CUtensorMap km, vm;
+  if (!encode_cache_map(&km, key_cache, dtype, num_blocks, num_kv_heads, head_dim) ||
+      !encode_cache_map(&vm, value_cache, dtype, num_blocks, num_kv_heads, head_dim))
+    return PA_ERR_CUDA;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  WeightsArgs a{};
+  a.query = static_cast<const uint16_t*>(query);
+  a.out = static_cast<uint16_t*>(out);
+  a.weights = weights;
+  a.tmp_out = reinterpret_cast<float*>(w + l.off[0]);
+  a.part_m = reinterpret_cast<float*>(w + l.off[1]);
+  a.part_l = reinterpret_cast<float*>(w + l.off[2]);
+  a.logits = reinterpret_cast<float*>(w + l.off[3]);
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.scale_log2 = scale * kLog2e;
+  a.num_seqs = static_cast<int>(num_seqs);
+  a.num_heads = static_cast<int>(num_heads);
+  a.num_kv_heads = static_cast<int>(num_kv_heads);
+  a.group = static_cast<int>(num_heads / num_kv_heads);
+  a.max_blocks_per_seq = static_cast<int>(max_blocks_per_seq);
+  a.num_blocks = static_cast<int>(num_blocks);
+  a.max_tokens = static_cast<int>(max_tokens);
+  a.new_tokens = static_cast<int>(new_tokens);
+  a.parts = static_cast<int>(l.parts);
+  a.runs = static_cast<int>(runs);
+  cudaStream_t s = as_stream(stream);
+  const bool bf16 = dtype == PA_BF16, wide = a.group > 8;
+  if (head_dim == 64) {
+    if (bf16)
+      return wide ? launch_weights_t<64, true, 2>(km, vm, a, items, merge, s)
+                  : launch_weights_t<64, true, 1>(km, vm, a, items, merge, s);
+    return wide ? launch_weights_t<64, false, 2>(km, vm, a, items, merge, s)
+                : launch_weights_t<64, false, 1>(km, vm, a, items, merge, s);
+  }
+  if (bf16)
+    return wide ? launch_weights_t<128, true, 2>(km, vm, a, items, merge, s)
+                : launch_weights_t<128, true, 1>(km, vm, a, items, merge, s);
+  return wide ? launch_weights_t<128, false, 2>(km, vm, a, items, merge, s)
+              : launch_weights_t<128, false, 1>(km, vm, a, items, merge, s);
+}
+// <<< decode that adds up attention weights

@@ -1,0 +1,441 @@
+// pa_decode_weights.cuh -- paged decode attention that also adds up the weight
+// each cached token receives.
+//
+// For one query token per sequence and the G query heads of a KV head,
+//   z_gj = scale q_g . k_j,   p_gj = exp(z_gj - lse_g),   lse_g = log sum_j exp(z_gj),
+//   out_g = sum_j p_gj v_j,   weights_j += sum_g p_gj.
+// The weights need lse_g, which is known only after the last token, and the
+// K rows are far larger than the logits (2 D bytes a token against 4 G): so
+// the pass over K and V leaves its logits in scratch memory, and a second,
+// small pass turns them into weights.
+//
+//   weights_split_kernel  one CTA per (sequence, KV head, partition of
+//     kWeightsPart tokens): the page pipeline and the transposed page step of
+//     the split decode (tokens and head dims as the mma's rows, heads as its
+//     columns, one or two column tiles of 8), with the logits written out.
+//   weights_merge_kernel  S x H CTAs merge the partitions' O by log-sum-exp;
+//     the others take a run of tokens each, find the heads' lse from the
+//     partitions' maxima and sums, and add the weights up.
+#pragma once
+
+#include "pa_decode.cuh"
+
+namespace pa {
+
+constexpr int kWeightsPart = 512;          // tokens per partition
+constexpr int kWeightsRun = 1024;          // tokens per CTA of the second pass
+constexpr int kWeightsThreads = 256;
+constexpr int kWeightsBatch = 8;           // partitions of O loaded before any is used
+
+struct WeightsArgs {
+  const uint16_t* query;         // [S, H, D]
+  uint16_t* out;                 // [S, H, D]
+  float* weights;                // [S, Hk, max_tokens]
+  float* tmp_out;                // [S, H, P, D] partition sums of p v, p against the partition's max
+  float* part_m;                 // [S, H, P] partition max, log2 units
+  float* part_l;                 // [S, H, P] partition sum of p
+  float* logits;                 // [S, Hk, MB * 16, G] z in log2 units
+  const int32_t* block_tables;   // [S, MB]
+  const int32_t* context_lens;   // [S]
+  float scale_log2;
+  int num_seqs;
+  int num_heads;
+  int num_kv_heads;
+  int group;
+  int max_blocks_per_seq;
+  int num_blocks;
+  int max_tokens;
+  int new_tokens;
+  int parts;                     // P
+  int runs;                      // CTAs per (sequence, KV head) that add weights up
+};
+
+// ---------------------------------------------------------------------------
+// Per-warp state and page step: S^T = K Q^T, O^T = V^T P^T for NT tiles of 8
+// query heads, the logits of the page's tokens written to z.  bf16 P goes in
+// as a hi + lo pair; the reference max may trail the true one by 2^kSlack.
+// ---------------------------------------------------------------------------
+template <int D, bool BF16, int NT>
+struct WeightsWarp {
+  static constexpr int KSTEPS = D / 16;
+  static constexpr int MTILES = D / 16;
+  static constexpr float kSlack = 8.f;
+  uint32_t qb[KSTEPS][NT][2];   // Q^T B fragments of query row 8 n + lane / 4
+  float acc[MTILES][NT][4];     // O^T: (dim 16c + g, rows 8n + 2t, + 1), (dim 16c + 8 + g, ...)
+  float m[NT][2], l[NT][2], mt[NT][2];
+
+  __device__ __forceinline__ void init(const uint16_t* q_group, int group, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = 8 * n + g;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(q_group + row * D);
+#pragma unroll
+      for (int kk = 0; kk < KSTEPS; ++kk) {
+        qb[kk][n][0] = row < group ? q[(kk * 16 + 2 * t) >> 1] : 0u;
+        qb[kk][n][1] = row < group ? q[(kk * 16 + 8 + 2 * t) >> 1] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < MTILES; ++i)
+        acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+      m[n][0] = m[n][1] = mt[n][0] = mt[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+  }
+
+  // z: the logits of the page's first token, `group` a token.
+  __device__ __forceinline__ void page(uint32_t kbase, uint32_t vbase, int lim, float scale_log2,
+                                       int lane, float* z, int group) {
+    const int g = lane >> 2, t = lane & 3;
+    const int ktok = (lane & 7) + ((lane >> 3) & 1) * 8;
+    const int kchk = lane >> 4;
+    float s[NT][2][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][0][i] = s[n][1][i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KSTEPS; ++kk) {
+      uint32_t a[4];
+      ldsm_x4(page_chunk<D>(kbase, ktok, 2 * kk + kchk), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_16816<BF16>(s[n][kk & 1], a, qb[kk][n][0], qb[kk][n][1]);
+    }
+    const bool lo_live = g < lim, hi_live = g + 8 < lim;
+    const bool odd = g & 1;
+    float x[NT][4];
+    bool grow = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      x[n][0] = lo_live ? (s[n][0][0] + s[n][1][0]) * scale_log2 : -INFINITY;
+      x[n][1] = lo_live ? (s[n][0][1] + s[n][1][1]) * scale_log2 : -INFINITY;
+      x[n][2] = hi_live ? (s[n][0][2] + s[n][1][2]) * scale_log2 : -INFINITY;
+      x[n][3] = hi_live ? (s[n][0][3] + s[n][1][3]) * scale_log2 : -INFINITY;
+      const int row = 8 * n + 2 * t;
+      if (row + 1 < group && !(group & 1)) {
+        if (lo_live) *reinterpret_cast<float2*>(z + g * group + row) = make_float2(x[n][0], x[n][1]);
+        if (hi_live)
+          *reinterpret_cast<float2*>(z + (g + 8) * group + row) = make_float2(x[n][2], x[n][3]);
+      } else {
+        if (row < group) {
+          if (lo_live) z[g * group + row] = x[n][0];
+          if (hi_live) z[(g + 8) * group + row] = x[n][2];
+        }
+        if (row + 1 < group) {
+          if (lo_live) z[g * group + row + 1] = x[n][1];
+          if (hi_live) z[(g + 8) * group + row + 1] = x[n][3];
+        }
+      }
+      // row maxima over the page: each lane reduces one of its two rows over
+      // the 8 lanes of equal t, the other comes from the neighbour
+      float keep = odd ? fmaxf(x[n][1], x[n][3]) : fmaxf(x[n][0], x[n][2]);
+      const float send = odd ? fmaxf(x[n][0], x[n][2]) : fmaxf(x[n][1], x[n][3]);
+      keep = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+      keep = fmaxf(keep, __shfl_xor_sync(0xffffffffu, keep, 8));
+      keep = fmaxf(keep, __shfl_xor_sync(0xffffffffu, keep, 16));
+      const float other = __shfl_xor_sync(0xffffffffu, keep, 4);
+      mt[n][0] = fmaxf(mt[n][0], odd ? other : keep);
+      mt[n][1] = fmaxf(mt[n][1], odd ? keep : other);
+      grow |= (mt[n][0] > m[n][0] + kSlack) | (mt[n][1] > m[n][1] + kSlack);
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // (a row of logits that are all -inf so far keeps a reference of -inf)
+          const float al = mt[n][h] > -INFINITY ? ex2(m[n][h] - mt[n][h]) : 1.f;
+          m[n][h] = mt[n][h];
+          l[n][h] *= al;
+#pragma unroll
+          for (int i = 0; i < MTILES; ++i) {
+            acc[i][n][h] *= al;
+            acc[i][n][2 + h] *= al;
+          }
+        }
+      }
+    }
+    uint32_t pb[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+      const float r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+      const float p0 = ex2(x[n][0] - r0), p1 = ex2(x[n][1] - r1);
+      const float p2 = ex2(x[n][2] - r0), p3 = ex2(x[n][3] - r1);
+      const uint32_t h_lo = pack2<BF16>(p0, p1), h_hi = pack2<BF16>(p2, p3);
+      pb[n][0] = movmatrix_trans(h_lo);
+      pb[n][1] = movmatrix_trans(h_hi);
+      if constexpr (BF16) {
+        const float2 u = unpack2<true>(h_lo), w = unpack2<true>(h_hi);
+        pb[n][2] = movmatrix_trans(pack2<true>(p0 - u.x, p1 - u.y));
+        pb[n][3] = movmatrix_trans(pack2<true>(p2 - w.x, p3 - w.y));
+      }
+      // l sums the fp32 p: the weights are exp(z - lse) of the same p
+      l[n][0] += p0 + p2;
+      l[n][1] += p1 + p3;
+    }
+    const int vtok = (lane & 7) + (lane >> 4) * 8;
+    const int vchk = (lane >> 3) & 1;
+#pragma unroll
+    for (int c = 0; c < MTILES; ++c) {
+      uint32_t a[4];
+      ldsm_x4_trans(page_chunk<D>(vbase, vtok, 2 * c + vchk), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_16816<BF16>(acc[c][n], a, pb[n][0], pb[n][1]);
+        if constexpr (BF16) mma_16816<BF16>(acc[c][n], a, pb[n][2], pb[n][3]);
+      }
+    }
+  }
+
+  // Rows < group into the merge buffers, restated against the true max.
+  __device__ __forceinline__ void publish(float* red_acc, float* red_m, float* red_l, int group,
+                                          int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = mt[n][h] > -INFINITY ? ex2(m[n][h] - mt[n][h]) : 1.f;
+        float lh = l[n][h] * f;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) lh += __shfl_xor_sync(0xffffffffu, lh, o);
+        const int row = 8 * n + 2 * t + h;
+        if (row < group) {
+#pragma unroll
+          for (int c = 0; c < MTILES; ++c) {
+            red_acc[row * D + 16 * c + g] = acc[c][n][h] * f;
+            red_acc[row * D + 16 * c + 8 + g] = acc[c][n][2 + h] * f;
+          }
+          if (g == 0) {
+            red_m[row] = mt[n][h];
+            red_l[row] = lh;
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int D, int NST, bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads)
+    weights_split_kernel(const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const WeightsArgs a) {
+  using L = DecodeSmem<D, NST>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  prefetch_tensormap(&kmap);
+  prefetch_tensormap(&vmap);
+  pdl_launch_dependents();
+  pdl_wait();
+
+  int item = blockIdx.x;
+  const int part = item % a.parts;
+  item /= a.parts;
+  const int kvh = item % a.num_kv_heads, s = item / a.num_kv_heads;
+  const int cap = a.max_blocks_per_seq * kPage;
+  int ctx = a.context_lens[s];
+  if (ctx < 0 || ctx > cap) {
+    if (threadIdx.x == 0 && part == 0 && kvh == 0) record_error(kErrContextLen, s);
+    ctx = ctx < 0 ? 0 : cap;
+  }
+  const int t_begin = part * kWeightsPart, t_end = min(t_begin + kWeightsPart, ctx);
+  if (t_begin >= t_end) return;
+  const int group = a.group;
+  const int first_page = t_begin / kPage;
+  const int n_pages = (t_end - t_begin + kPage - 1) / kPage;   // <= 32: one id a lane
+  const int my_pages = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;
+  const uint32_t stage0 = smem_addr(smem) + warp * NST * L::kStageBytes;
+  const uint32_t bar0 = smem_addr(smem + L::kBarOffset) + warp * NST * 8;
+  init_ring<NST>(bar0, lane);
+
+  static_assert(kWeightsPart / kPage <= 32, "the pages of a partition: one id a lane");
+  int id = -1;
+  if (lane < n_pages) {
+    const size_t at = static_cast<size_t>(s) * a.max_blocks_per_seq + first_page + lane;
+    id = a.block_tables[at];
+    if (id < 0 || id >= a.num_blocks) {
+      if (warp == 0) record_error(kErrBlockId, static_cast<long long>(at));
+      id = -1;   // a box at a negative row reads zeros
+    }
+  }
+  auto issue = [&](int k) {   // whole warp; lane 0 loads this warp's page k
+    const int row = __shfl_sync(0xffffffffu, id, warp + k * kWarps) * kPage;
+    if (lane == 0) {
+      const uint32_t bar = bar0 + (k % NST) * 8;
+      const uint32_t dk = stage0 + (k % NST) * L::kStageBytes, dv = dk + L::kPageBytes;
+      mbar_arrive_expect_tx(bar, L::kStageBytes);
+#pragma unroll
+      for (int b = 0; b < L::kBoxesPerRow; ++b)
+        tma_load_4d(dk + b * kBoxBytes, &kmap, bar, 0, b, kvh, row);
+#pragma unroll
+      for (int b = 0; b < L::kBoxesPerRow; ++b)
+        tma_load_4d(dv + b * kBoxBytes, &vmap, bar, 0, b, kvh, row);
+    }
+  };
+  for (int k = 0; k < min(my_pages, NST); ++k) issue(k);
+
+  WeightsWarp<D, BF16, NT> st;
+  st.init(a.query + (static_cast<size_t>(s) * a.num_heads + static_cast<size_t>(kvh) * group) * D,
+          group, lane);
+  float* z = a.logits + (static_cast<size_t>(s) * a.num_kv_heads + kvh) * cap * group;
+  bool ok = true;
+  int k_stop = my_pages;
+  for (int k = 0; k < my_pages; ++k) {
+    if (!__all_sync(~0u, mbar_wait_bounded(bar0 + (k % NST) * 8, (k / NST) & 1))) {
+      if (lane == 0) record_error(kErrWaitTimeout, blockIdx.x);
+      ok = false;
+      k_stop = k;
+      break;
+    }
+    const uint32_t kb = stage0 + (k % NST) * L::kStageBytes;
+    const int tok0 = t_begin + (warp + k * kWarps) * kPage;
+    if (tok0 + kPage > ctx) zero_page_tail<L::kBoxesPerRow>(kb + L::kPageBytes, ctx - tok0, lane);
+    st.page(kb, kb + L::kPageBytes, t_end - tok0, a.scale_log2, lane,
+            z + static_cast<size_t>(tok0) * group, group);
+    __syncwarp();
+    if (k + NST < my_pages) issue(k + NST);
+  }
+  // (a warp that gave up first waits for the loads it still has in flight)
+  if (!__syncthreads_and(drain_stages<NST>(ok, k_stop, my_pages, bar0))) return;
+  float* red_acc = reinterpret_cast<float*>(smem);
+  float* red_m = reinterpret_cast<float*>(smem + L::kRedMOffset);
+  float* red_l = reinterpret_cast<float*>(smem + L::kRedLOffset);
+  if (ok) {
+    st.publish(red_acc + warp * group * D, red_m + warp * 16, red_l + warp * 16, group, lane);
+  } else {
+    for (int g = lane; g < group; g += 32) {
+      red_m[warp * 16 + g] = -INFINITY;
+      red_l[warp * 16 + g] = 0.f;
+    }
+  }
+  __syncthreads();
+  const size_t hrow0 = static_cast<size_t>(s) * a.num_heads + static_cast<size_t>(kvh) * group;
+  merge_and_emit<D, NST>(smem, group, false, 1, 0,
+                         [&](int g, int d, float o0, float o1, float big_m, float big_l) {
+    const size_t p = (hrow0 + g) * a.parts + part;
+    *reinterpret_cast<float2*>(a.tmp_out + p * D + d) = make_float2(o0, o1);
+    if (d == 0) {
+      a.part_m[p] = big_m;
+      a.part_l[p] = big_l;
+    }
+  });
+}
+
+// lse (log2 units) of one head from its partitions, whole warp; +inf when no
+// token has a finite logit, so that every weight comes out 0.
+__device__ __forceinline__ float warp_lse(const float* m, const float* l, int np, int lane) {
+  float big = -INFINITY;
+  for (int p = lane; p < np; p += 32) big = fmaxf(big, m[p]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+  const float ref = big == -INFINITY ? 0.f : big;
+  float sum = 0.f;
+  for (int p = lane; p < np; p += 32) sum += ex2(m[p] - ref) * l[p];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum == 0.f ? INFINITY : ref + __log2f(sum);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kWeightsThreads)
+    weights_merge_kernel(const WeightsArgs a) {
+  __shared__ float4 acc_sh[kWeightsThreads];
+  __shared__ float lse_sh[kWeightsThreads / 32 * 2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cap = a.max_blocks_per_seq * kPage;
+  const int rows = a.num_seqs * a.num_heads;
+  int b = blockIdx.x;
+  if (b < rows) {
+    // ---- O of one (sequence, head) ----
+    const int ctx = min(max(a.context_lens[b / a.num_heads], 0), cap);
+    const int np = (ctx + kWeightsPart - 1) / kWeightsPart;
+    const size_t base = static_cast<size_t>(b) * a.parts;
+    if (warp == 0) {
+      const float lse = warp_lse(a.part_m + base, a.part_l + base, np, lane);
+      if (lane == 0) lse_sh[0] = lse;
+    }
+    __syncthreads();
+    const float lse = lse_sh[0];
+    constexpr int kQuads = D / 4, kGroups = kWeightsThreads / kQuads;
+    const int q = tid % kQuads, grp = tid / kQuads;
+    const float4* src = reinterpret_cast<const float4*>(a.tmp_out + base * D) + q;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = grp; p0 < np; p0 += kGroups * kWeightsBatch) {
+      float4 v[kWeightsBatch];
+      float f[kWeightsBatch];
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) {
+        const int p = p0 + u * kGroups;
+        f[u] = p < np ? a.part_m[base + p] : -INFINITY;
+        v[u] = p < np ? src[static_cast<size_t>(p) * kQuads] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) {
+        const float e = ex2(f[u] - lse);
+        acc.x += e * v[u].x;
+        acc.y += e * v[u].y;
+        acc.z += e * v[u].z;
+        acc.w += e * v[u].w;
+      }
+    }
+    acc_sh[tid] = acc;
+    __syncthreads();
+    if (tid < kQuads) {
+      for (int g = 1; g < kGroups; ++g) {
+        const float4 u = acc_sh[g * kQuads + tid];
+        acc.x += u.x;
+        acc.y += u.y;
+        acc.z += u.z;
+        acc.w += u.w;
+      }
+      uint2 r;
+      r.x = pack2<BF16>(acc.x, acc.y);
+      r.y = pack2<BF16>(acc.z, acc.w);
+      *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(b) * D + tid * 4) = r;
+    }
+    return;
+  }
+  // ---- the weights of a run of tokens ----
+  b -= rows;
+  const int run = b % a.runs, row = b / a.runs;        // row = s * Hk + kv
+  const int s = row / a.num_kv_heads, kv = row % a.num_kv_heads;
+  const int ctx = min(max(a.context_lens[s], 0), cap);
+  if (ctx > a.max_tokens) {
+    if (tid == 0 && run == 0 && kv == 0) record_error(kErrContextLen, s);
+    return;
+  }
+  const int t0 = run * kWeightsRun, t1 = min(t0 + kWeightsRun, ctx);
+  if (t0 >= t1) return;
+  const int np = (ctx + kWeightsPart - 1) / kWeightsPart;
+  const int G = a.group;
+  for (int g = warp; g < G; g += kWeightsThreads / 32) {
+    const size_t base = (static_cast<size_t>(s) * a.num_heads + kv * G + g) * a.parts;
+    const float lse = warp_lse(a.part_m + base, a.part_l + base, np, lane);
+    if (lane == 0) lse_sh[g] = lse;
+  }
+  __syncthreads();
+  const float* z = a.logits + static_cast<size_t>(row) * cap * G;
+  float* w = a.weights + static_cast<size_t>(row) * a.max_tokens;
+  const int fresh = max(ctx - a.new_tokens, 0);        // tokens from here on start anew
+  for (int t = t0 + tid; t < t1; t += kWeightsThreads) {
+    const float* zt = z + static_cast<size_t>(t) * G;
+    float sum = 0.f;
+    if ((G & 3) == 0) {
+      for (int g = 0; g < G; g += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(zt + g);
+        sum += (ex2(v.x - lse_sh[g]) + ex2(v.y - lse_sh[g + 1])) +
+               (ex2(v.z - lse_sh[g + 2]) + ex2(v.w - lse_sh[g + 3]));
+      }
+    } else {
+      for (int g = 0; g < G; ++g) sum += ex2(zt[g] - lse_sh[g]);
+    }
+    w[t] = t < fresh ? w[t] + sum : sum;
+  }
+}
+
+}  // namespace pa

@@ -74,3 +74,32 @@ def test_binding_refuses_wrong_tensors():
                 dict(block_tables=i32(2, 4)[:, ::2]), {}):
         with pytest.raises(ValueError):
             pa_evict_compact(**{**good, **more, **bad})
+
+
+WEIGHTS_ORDER = ("out weights ws ws_bytes query kc vc bt ctx scale S H Hk D NB bs MB W new "
+                 "dt").split()
+WEIGHTS_BASE = dict({k: FAKE for k in ("out", "weights", "ws", "query", "kc", "vc", "bt", "ctx")},
+                    ws_bytes=1 << 30, scale=0.1, S=4, H=8, Hk=2, D=128, NB=64, bs=16, MB=8, W=128,
+                    new=1, dt=0)
+
+
+@host_only
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dt=7)), (SHAPE, dict(S=-1)), (SHAPE, dict(H=7)), (SHAPE, dict(W=0)),
+    (SHAPE, dict(new=-1)), (SHAPE, dict(ws_bytes=100)), (SHAPE, dict(scale=float("inf"))),
+    (NULL, dict(weights=None)), (NULL, dict(ws=None)), (NULL, dict(out=None)),
+    (ALIGN, dict(ws=FAKE + 128)), (ALIGN, dict(weights=FAKE + 2)), (ALIGN, dict(out=FAKE + 8)),
+    (UNSUP, dict(D=96)), (UNSUP, dict(bs=8)), (UNSUP, dict(H=64, Hk=2)),
+    (OK, dict(S=0, ws=None)), (CUDA, dict()),
+])
+def test_decode_weights_refusals(want, kw):
+    assert _call("pa_decode_weights", WEIGHTS_ORDER, WEIGHTS_BASE, **kw) == want
+
+
+def test_decode_weights_workspace_bytes():
+    f = _lib.load().pa_decode_weights_workspace_bytes
+    # 4 x 8 rows of one 512-token partition (D + 2 floats), 128 logits each
+    assert f(4, 8, 128, 8, 16) == 32 * 128 * 4 + 256 + 256 + 32 * 128 * 4
+    assert f(0, 8, 128, 8, 16) == 0
+    for bad in ((-1, 8, 128, 8, 16), (1, 0, 128, 8, 16), (1, 8, 0, 8, 16), (1, 8, 128, 0, 16)):
+        assert f(*bad) == -1

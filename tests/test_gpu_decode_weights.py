@@ -1,0 +1,213 @@
+"""pa_decode_weights against attention and its weights in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_cache_444_b200 import (PagedAttentionError, WeightsWorkspace, pa_check_error,
+                                     pa_decode, pa_decode_weights, workloads)
+from parity_helpers import grow_logits, poison_past_context
+from weights_reference import attend, out_bound
+
+pytestmark = pytest.mark.gpu
+BASE = workloads.CONFIGS["gqa_llama3_8b"]
+
+
+def _batch(dev, ctx, heads, kv_heads, dim, dtype, seed):
+    blocks = sum(-(-c // 16) for c in ctx) + 2
+    return workloads.make_batch(BASE.scaled(
+        name="w", num_seqs=len(ctx), num_heads=heads, num_kv_heads=kv_heads, head_dim=dim,
+        dtype=dtype, num_blocks=blocks, ctx=("fixed", tuple(ctx)), seed=seed), dev)
+
+
+def _call(b, weights, new_tokens=1, scale=None, ws=None, stream=None, out=None):
+    out = torch.full_like(b.query, float("nan")) if out is None else out
+    ws = ws or WeightsWorkspace.for_call(b.query, b.key_cache, b.block_tables)
+    pa_decode_weights(out, weights, ws, b.query, b.key_cache, b.value_cache, b.block_tables,
+                      b.context_lens, b.cfg.scale if scale is None else scale, new_tokens, stream)
+    return out
+
+
+def _check(b, before, after, out, new_tokens, scale):
+    cfg, G = b.cfg, b.cfg.group_size
+    p_half = 2.0 ** -16 if cfg.dtype == "bf16" else 2.0 ** -11
+    for s, n in enumerate(b.context_lens.tolist()):
+        if n == 0:
+            assert (out[s] == 0).all()
+            assert torch.equal(after[s].view(torch.int32), before[s].view(torch.int32))
+            continue
+        at = torch.arange(n, device=out.device)
+        blk, row = b.block_tables[s, at // 16].long(), at % 16
+        for kv in range(cfg.num_kv_heads):
+            k, v = b.key_cache[blk, row, kv], b.value_cache[blk, row, kv]
+            q = b.query[s, kv * G:(kv + 1) * G]
+            p, o, _, rel, pv = attend(q, k, v, scale)
+            err = (out[s, kv * G:(kv + 1) * G].double() - o).abs()
+            lim = out_bound(o, pv, rel, n, float(v.double().abs().max()), out.dtype, p_half)
+            assert (err <= lim).all(), (s, kv, float((err / lim).max()))
+            fresh = max(0, n - new_tokens)
+            old = before[s, kv, :n].double().clone()
+            old[fresh:] = 0
+            want = old + p.sum(0)
+            err = (after[s, kv, :n].double() - want).abs()
+            lim = (p * rel[:, None]).sum(0) + (G + 2) * 2.0 ** -24 * want.abs() + 1e-37
+            assert (err <= lim).all(), (s, kv, float((err / lim).max()))
+        assert torch.equal(after[s, :, n:].view(torch.int32), before[s, :, n:].view(torch.int32))
+
+
+CASES = {
+    # name: (contexts, heads, KV heads, head_dim, dtype, new tokens, weight columns over the longest)
+    "one_token": ((1,), 1, 1, 64, "f16", 1, 0),
+    "tiny": ((1, 9, 16, 37), 4, 4, 64, "f16", 1, 3),
+    "empty_between": ((0, 17, 0, 33), 8, 2, 128, "bf16", 1, 1),
+    "partition_edges": ((511, 512, 513, 1023, 1025), 8, 2, 128, "bf16", 1, 7),
+    "group3": ((45, 700), 12, 4, 128, "f16", 1, 0),
+    "group2_bf16_d64": ((130, 1), 4, 2, 64, "bf16", 1, 5),
+    "group8": ((600, 31), 16, 2, 128, "f16", 2, 0),
+    "group9": ((64, 530), 9, 1, 128, "bf16", 1, 0),
+    "group12_d64": ((300,), 12, 1, 64, "f16", 1, 2),
+    "group16": ((515, 18), 32, 2, 128, "bf16", 1, 0),
+    "mha": ((200, 77), 8, 8, 128, "f16", 1, 0),
+    "nothing_new": ((100, 20), 8, 2, 128, "bf16", 0, 0),
+    "all_new": ((100, 20), 8, 2, 128, "bf16", 1000, 0),
+    "long": ((9000, 4097), 8, 2, 128, "bf16", 1, 11),
+    "long_mha_d64": ((5001,), 2, 2, 64, "f16", 16, 0),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_matches_the_definition(name, cuda_device):
+    ctx, H, Hk, D, dtype, new, extra = CASES[name]
+    b = _batch(cuda_device, ctx, H, Hk, D, dtype, 900 + len(name))
+    poison_past_context(b)           # rows and weights past a context are never used
+    weights = torch.rand((len(ctx), Hk, max(ctx) + extra), device=cuda_device)
+    for s, n in enumerate(ctx):
+        weights[s, :, max(0, n - new):] = float("nan")
+    before = weights.clone()
+    out = _call(b, weights, new)
+    torch.cuda.synchronize()
+    pa_check_error()
+    _check(b, before, weights, out, new, b.cfg.scale)
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 8), ("f16", 8), ("bf16", 20)])
+def test_climbing_logits(dtype, heads, cuda_device):
+    """Row maxima that outgrow the reference several times within a partition."""
+    b = _batch(cuda_device, (1500, 300), heads, 2, 128, dtype, 931)
+    grow_logits(b)
+    weights = torch.zeros((2, 2, 1500), device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights)
+    torch.cuda.synchronize()
+    pa_check_error()
+    _check(b, before, weights, out, 1, b.cfg.scale)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_other_scales(scale, cuda_device):
+    b = _batch(cuda_device, (700, 33), 8, 2, 64, "bf16", 932)
+    weights = torch.zeros((2, 2, 700), device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights, scale=scale)
+    torch.cuda.synchronize()
+    _check(b, before, weights, out, 1, scale)
+
+
+def test_steps_add_up_to_the_number_of_heads(cuda_device):
+    """Three steps over one cache: each adds the group's heads' weight of 1 to every KV head;
+    the output is that of pa_decode up to the rounding of P."""
+    b = _batch(cuda_device, (777, 1200, 5), 32, 8, 128, "f16", 933)
+    ws = WeightsWorkspace.for_call(b.query, b.key_cache, b.block_tables)
+    weights = torch.zeros((3, 8, 1200), device=cuda_device)
+    out = torch.empty_like(b.query)
+    for _ in range(3):
+        _call(b, weights, 0, ws=ws, out=out)
+    torch.cuda.synchronize()
+    total = weights.double().sum(-1)
+    # each p is off by rel < 2^-10 at these sizes (module bound), in sum by its mean
+    assert (total - 12).abs().max() < 12 * 2.0 ** -10
+    plain = torch.empty_like(out)
+    pa_decode(plain, b.query, b.key_cache, b.value_cache, b.block_tables, b.context_lens,
+              b.cfg.scale)
+    assert (plain.float() - out.float()).abs().max() < 2e-3
+    pa_check_error()
+
+
+def test_nan_and_infinite_values_stay_with_their_own_sequence(cuda_device):
+    b = _batch(cuda_device, (100, 100, 100), 4, 2, 64, "bf16", 934)
+    k_nan, v_inf = int(b.block_tables[0, 2]), int(b.block_tables[1, 3])
+    b.key_cache[k_nan, 3, 0] = float("nan")
+    b.value_cache[v_inf, 1, 1, 5] = float("inf")
+    weights = torch.zeros((3, 2, 100), device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights)
+    torch.cuda.synchronize()
+    assert out[0, :2].isnan().all() and weights[0, 0].isnan().all()
+    assert out[0, 2:].isfinite().all() and weights[0, 1].isfinite().all()
+    # (bf16 P enters as a hi + lo pair, and lo may be 0 or negative: inf or NaN, as pa_decode)
+    assert not out[1, 2:, 5].isfinite().any() and weights[1].isfinite().all()
+    rest = out[1].clone()
+    rest[2:, 5] = 0
+    assert rest.isfinite().all()
+    b.context_lens[:2] = 0            # check the third alone
+    before[:2], weights[:2], out[:2] = 0, 0, 0
+    _check(b, before, weights, out, 1, b.cfg.scale)
+
+
+def test_reports_bad_lengths_and_blocks(cuda_device):
+    b = _batch(cuda_device, (40, 60, 20), 4, 2, 64, "f16", 935)
+    weights = torch.full((3, 2, 50), 0.5, device=cuda_device)      # 60 does not fit
+    before = weights.clone()
+    out = _call(b, weights)
+    with pytest.raises(PagedAttentionError, match="context_len, index 1"):
+        pa_check_error()
+    assert torch.equal(weights[1], before[1])
+    plain = torch.empty_like(out)
+    pa_decode(plain, b.query, b.key_cache, b.value_cache, b.block_tables, b.context_lens,
+              b.cfg.scale)
+    assert (plain.float() - out.float()).abs().max() < 2e-3
+    wide = torch.zeros((3, 2, 64), device=cuda_device)
+    b.block_tables[2, 1] = 1 << 20
+    _call(b, wide)
+    with pytest.raises(PagedAttentionError, match="block_id, index 9"):
+        pa_check_error()
+    assert wide.isfinite().all()
+    pa_check_error()
+
+
+def test_graph_and_another_stream(cuda_device):
+    b = _batch(cuda_device, (300, 40), 8, 2, 128, "bf16", 936)
+    ws = WeightsWorkspace.for_call(b.query, b.key_cache, b.block_tables)
+    weights = torch.zeros((2, 2, 320), device=cuda_device)
+    out = torch.empty_like(b.query)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    _call(b, weights, ws=ws, out=out, stream=side)
+    side.synchronize()
+    _check(b, torch.zeros_like(weights), weights, out, 1, b.cfg.scale)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _call(b, weights, ws=ws, out=out)
+    for seed in (1, 2):
+        b.query.normal_(generator=torch.Generator(device=cuda_device).manual_seed(seed))
+        before = weights.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        _check(b, before, weights, out, 1, b.cfg.scale)
+    pa_check_error()
+
+
+def test_workspace_too_small_is_refused(cuda_device):
+    b = _batch(cuda_device, (300, 40), 8, 2, 128, "bf16", 937)
+    weights = torch.zeros((2, 2, 320), device=cuda_device)
+    small = WeightsWorkspace(1, 8, 128, b.block_tables.shape[1], cuda_device)
+    with pytest.raises(PagedAttentionError, match="PA_ERR_SHAPE"):
+        _call(b, weights, ws=small)
+    assert (weights == 0).all()
+    with pytest.raises(ValueError):
+        _call(b, weights.double())
+    with pytest.raises(ValueError):
+        _call(b, weights[:, :1])
+    with pytest.raises(PagedAttentionError, match="PA_ERR_SHAPE"):
+        _call(b, weights, new_tokens=-1)
+    assert math.isfinite(float(weights.sum()))
