@@ -69,7 +69,8 @@ enum {
     PA_CHECK_PARTITIONS = 4,    /* ceil(context_lens[s]/partition_size) > max_partitions; index = s */
     PA_CHECK_WAIT_TIMEOUT = 5,  /* a shared-memory barrier wait gave up; index = CTA id */
     PA_CHECK_GROUP = 6,         /* malformed group bounds or prefix length; index = group */
-    PA_CHECK_QUERY = 7,         /* prefill: q_len < 0, q_len > context_lens[s] or context too long; index = s */
+    PA_CHECK_QUERY = 7,         /* prefill: q_len < 0, q_len > context_lens[s] or context too long;
+                                   prompt: seq_starts[s .. s+1] not ascending within the tokens; index = s */
     PA_CHECK_VALUE = 8,         /* prefill, bf16: a V value beyond the fp16 range was clamped to +-65504; index = s */
     PA_CHECK_SOURCE = 9         /* evict: source[i] neither i nor a slot in [new_lens[s], context_lens[s]);
                                    index = (s*num_kv_heads + kv)*budget + i */
@@ -338,6 +339,35 @@ pa_status pa_prefill(void *out, const void *query, const void *key_cache,
                      int64_t num_heads, int64_t num_kv_heads, int64_t head_dim,
                      int64_t num_blocks, int64_t block_size, int64_t max_blocks_per_seq,
                      pa_dtype dtype, void *stream);
+
+/*
+ * pa_prompt_attention -- causal attention over whole prompts, before (or beside)
+ * their rows' way into the cache: nothing is gathered through block tables.
+ *   query      [num_tokens, num_heads, head_dim], key and value
+ *              [num_tokens, num_kv_heads, head_dim]: the sequences' tokens packed
+ *              one after another; consecutive tokens query_stride / key_stride /
+ *              value_stride ELEMENTS apart (at least the row, a multiple of 8), so
+ *              the rows of one fused projection can be given as they are
+ *   seq_starts [num_seqs + 1] int32: sequence s is tokens seq_starts[s] ..
+ *              seq_starts[s+1] - 1 (it may be empty)
+ *   out        [num_tokens, num_heads, head_dim] (written, dense)
+ *   lse        [num_tokens, num_heads] fp32 (written) or NULL:
+ *              log sum_j exp(scale * q.k_j) over the keys the token sees
+ * Token i of a sequence attends to its tokens 0..i.  fp32 accumulation and softmax
+ * statistics, P rounded to dtype, the output rounded once.  Rows of out and lse
+ * that belong to no sequence are left as they were.  What a token does not see
+ * (later tokens, other sequences) does not reach it, NaN and infinities included; a
+ * row whose logits are all -inf gives zeros and lse = -inf.  A sequence whose
+ * bounds are not 0 <= start <= end <= num_tokens is left out and reported
+ * (PA_CHECK_QUERY, index = s).  head_dim in {64, 128}, at most 16 query heads per
+ * KV head.
+ */
+pa_status pa_prompt_attention(void *out, float *lse, const void *query, const void *key,
+                              const void *value, int64_t query_stride, int64_t key_stride,
+                              int64_t value_stride, const int32_t *seq_starts, float scale,
+                              int64_t num_seqs, int64_t num_tokens, int64_t num_heads,
+                              int64_t num_kv_heads, int64_t head_dim, pa_dtype dtype,
+                              void *stream);
 
 /*
  * pa_decode_weights -- pa_decode that also adds up what each cached token

@@ -71,6 +71,7 @@ SIGNATURES = {
     "pa_decode_step_host_workspace_bytes": (_i64, [_i64] * 7),
     "pa_decode_step_host": (_i, [_p] * 10 + [_i64, _f] + [_i64] * 8 + [_i, _p]),
     "pa_prefill": (_i, [_p] * 7 + [_f] + [_i64] * 9 + [_i, _p]),
+    "pa_prompt_attention": (_i, [_p] * 5 + [_i64] * 3 + [_p, _f] + [_i64] * 5 + [_i, _p]),
     "pa_decode_weights_workspace_bytes": (_i64, [_i64] * 5),
     "pa_decode_weights": (_i, [_p] * 3 + [_i64] + [_p] * 5 + [_f] + [_i64] * 9 + [_i, _p]),
     "pa_evict_select": (_i, [_p] * 7 + [_i64] * 6 + [_p]),
@@ -383,6 +384,41 @@ def pa_prefill(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
                            int(max_query_len), H, Hk, D, NB, bs, block_tables.shape[1],
                            _dtype_code(query), _stream(stream))
     _check(st, "pa_prefill")
+
+
+def _prompt_rows(name, rows, T, D):
+    _need(rows.dim() == 3 and rows.shape[0] == T and rows.shape[2] == D,
+          f"{name} must be [num_tokens, heads, head_dim]")
+    _need(rows.stride()[1:] == (D, 1) or rows.numel() == 0, f"{name} token rows must be dense")
+    return rows.stride(0) if T > 1 else rows.shape[1] * D
+
+
+def pa_prompt_attention(out: torch.Tensor, lse: torch.Tensor | None, query: torch.Tensor,
+                        key: torch.Tensor, value: torch.Tensor, seq_starts: torch.Tensor,
+                        scale: float, stream=None) -> None:
+    """Causal attention over packed prompts: query [T, H, D], key/value
+    [T, Hk, D] (token rows may be strided), sequence s is rows seq_starts[s] to
+    seq_starts[s + 1] - 1; out [T, H, D], lse [T, H] float32 or None."""
+    T, H, D = query.shape
+    Hk = key.shape[1]
+    strides = [_prompt_rows(n, t, T, D) for n, t in
+               (("query", query), ("key", key), ("value", value))]
+    _need(value.shape == key.shape, "key/value shapes differ")
+    _need(query.dtype == key.dtype == value.dtype, "dtype mismatch")
+    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
+          "out must be [num_tokens, num_heads, head_dim] contiguous")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (T, H) and
+                          lse.is_contiguous()), "lse must be [num_tokens, num_heads] float32")
+    _need(seq_starts.dtype == torch.int32 and seq_starts.dim() == 1 and
+          seq_starts.shape[0] >= 1 and seq_starts.is_contiguous(),
+          "seq_starts must be [num_seqs + 1] int32")
+    dt = _dtype_code(query)
+    _on_one_device(stream, query, key, value, out, seq_starts, *([] if lse is None else [lse]))
+    st = load().pa_prompt_attention(out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                    query.data_ptr(), key.data_ptr(), value.data_ptr(), *strides,
+                                    seq_starts.data_ptr(), float(scale), seq_starts.shape[0] - 1,
+                                    T, H, Hk, D, dt, _stream(stream))
+    _check(st, "pa_prompt_attention")
 
 
 def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, workspace, query: torch.Tensor,

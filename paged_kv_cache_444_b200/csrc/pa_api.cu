@@ -1429,3 +1429,120 @@ extern "C" pa_status pa_decode_weights(void* out, float* weights, void* workspac
               : launch_weights_t<128, false, 1>(km, vm, a, items, merge, s);
 }
 // <<< decode that adds up attention weights
+
+// >>> whole-prompt attention (pa_prompt_attention): host side.
+#include "pa_prompt.cuh"
+
+namespace {
+// 4-D view of packed rows [T, heads, D], consecutive tokens `stride` elements
+// apart, for boxes of `box_heads` heads x `box_tokens` tokens x 64 elements
+// (128-byte swizzle; zero fill out of range).
+bool encode_rows_map(CUtensorMap* map, const void* rows, pa_dtype dtype, int64_t num_tokens,
+                     int64_t heads, int64_t head_dim, int64_t stride, int64_t box_heads,
+                     int64_t box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(head_dim / 64),
+                              static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(num_tokens)};
+  const cuuint64_t strides[3] = {128, static_cast<cuuint64_t>(head_dim * 2),
+                                 static_cast<cuuint64_t>(stride * 2)};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            4, const_cast<void*>(rows), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The sizes and scalars of a packed prompt (host only, no CUDA calls).
+pa_status check_prompt_sizes(float scale, int64_t num_seqs, int64_t num_tokens, int64_t num_heads,
+                             int64_t num_kv_heads, int64_t head_dim, pa_dtype dtype) {
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_DTYPE;
+  if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0)
+    return PA_ERR_SHAPE;
+  if (num_heads % num_kv_heads != 0 || !std::isfinite(scale)) return PA_ERR_SHAPE;
+  if (head_dim % 8 != 0) return PA_ERR_ALIGN;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (num_heads / num_kv_heads > 16) return PA_ERR_UNSUPPORTED;
+  // index ranges the kernels address with 32-bit ints
+  if (num_heads > 65535 || num_seqs > (1 << 30) || num_tokens > (1 << 30) ||
+      num_tokens * num_heads > INT32_MAX || num_seqs * num_heads > INT32_MAX)
+    return PA_ERR_SHAPE;
+  return PA_OK;
+}
+
+// One set of packed rows: `width` elements a token, tokens `stride` apart.
+pa_status check_prompt_rows(const void* rows, int64_t stride, int64_t width) {
+  if (!rows) return PA_ERR_NULL;
+  if (stride < width || stride > (1ll << 38)) return PA_ERR_SHAPE;
+  if (!aligned16(rows) || stride % 8 != 0) return PA_ERR_ALIGN;
+  return PA_OK;
+}
+
+template <int D, bool BF16>
+pa_status launch_prompt_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                          const PromptArgs& a, long long items, cudaStream_t stream) {
+  using L = PromptSmem<D>;
+  auto kernel = prompt_attention_kernel<D, BF16>;
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(kernel, L::kAlloc, &done)) return PA_ERR_CUDA;
+  const long long sms = sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  return launch_ex(kernel, static_cast<unsigned>(items < sms ? items : sms), kPromptThreads,
+                   L::kAlloc, stream, 1, qm, km, vm, a);
+}
+}  // namespace
+
+extern "C" pa_status pa_prompt_attention(void* out, float* lse, const void* query, const void* key,
+                                         const void* value, int64_t query_stride,
+                                         int64_t key_stride, int64_t value_stride,
+                                         const int32_t* seq_starts, float scale, int64_t num_seqs,
+                                         int64_t num_tokens, int64_t num_heads,
+                                         int64_t num_kv_heads, int64_t head_dim, pa_dtype dtype,
+                                         void* stream) {
+  pa_status st = check_prompt_sizes(scale, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                    dtype);
+  if (st != PA_OK) return st;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!out || !seq_starts) return PA_ERR_NULL;
+  if ((st = check_prompt_rows(query, query_stride, num_heads * head_dim)) != PA_OK) return st;
+  if ((st = check_prompt_rows(key, key_stride, num_kv_heads * head_dim)) != PA_OK) return st;
+  if ((st = check_prompt_rows(value, value_stride, num_kv_heads * head_dim)) != PA_OK) return st;
+  if (!aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(seq_starts) & 3u))
+    return PA_ERR_ALIGN;
+  const int64_t G = num_heads / num_kv_heads, tile = kPrefillRows / G;
+  const long long items = (num_tokens / (2 * tile) + num_seqs) * num_kv_heads;   // at most
+  if (items > INT32_MAX) return PA_ERR_SHAPE;
+  CUtensorMap qm, km, vm;
+  if (!encode_rows_map(&qm, query, dtype, num_tokens, num_heads, head_dim, query_stride, G, tile) ||
+      !encode_rows_map(&km, key, dtype, num_tokens, num_kv_heads, head_dim, key_stride, 1,
+                       kPrefillKeys) ||
+      !encode_rows_map(&vm, value, dtype, num_tokens, num_kv_heads, head_dim, value_stride, 1,
+                       kPrefillKeys))
+    return PA_ERR_CUDA;
+  PromptArgs a{};
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.value = static_cast<const uint16_t*>(value);
+  a.value_stride = value_stride;
+  a.seq_starts = seq_starts;
+  a.scale_log2 = scale * kLog2e;
+  a.num_seqs = static_cast<int>(num_seqs);
+  a.num_tokens = static_cast<int>(num_tokens);
+  a.num_heads = static_cast<int>(num_heads);
+  a.num_kv_heads = static_cast<int>(num_kv_heads);
+  a.group = static_cast<int>(G);
+  a.tile_tokens = static_cast<int>(tile);
+  cudaStream_t s = as_stream(stream);
+  const bool bf16 = dtype == PA_BF16;
+  if (head_dim == 64)
+    return bf16 ? launch_prompt_t<64, true>(qm, km, vm, a, items, s)
+                : launch_prompt_t<64, false>(qm, km, vm, a, items, s);
+  return bf16 ? launch_prompt_t<128, true>(qm, km, vm, a, items, s)
+              : launch_prompt_t<128, false>(qm, km, vm, a, items, s);
+}
+// <<< whole-prompt attention

@@ -103,3 +103,22 @@ def test_decode_weights_workspace_bytes():
     assert f(0, 8, 128, 8, 16) == 0
     for bad in ((-1, 8, 128, 8, 16), (1, 0, 128, 8, 16), (1, 8, 0, 8, 16), (1, 8, 128, 0, 16)):
         assert f(*bad) == -1
+
+
+PROMPT_ORDER = "out lse q k v qs ks vs starts scale S T H Hk D dt".split()
+PROMPT_BASE = dict({k: FAKE for k in ("out", "lse", "q", "k", "v", "starts")}, qs=1024, ks=256,
+                   vs=256, scale=0.1, S=3, T=100, H=8, Hk=2, D=128, dt=1)
+
+
+@host_only
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dt=2)), (SHAPE, dict(S=-1)), (SHAPE, dict(T=-1)), (SHAPE, dict(H=7)),
+    (SHAPE, dict(qs=1016)), (SHAPE, dict(ks=128)), (SHAPE, dict(T=1 << 29)),
+    (SHAPE, dict(scale=float("nan"))), (UNSUP, dict(D=96, qs=768)), (UNSUP, dict(H=64, Hk=2)),
+    (NULL, dict(out=None)), (NULL, dict(v=None)), (NULL, dict(starts=None)),
+    (ALIGN, dict(ks=260)), (ALIGN, dict(v=FAKE + 8)), (ALIGN, dict(lse=FAKE + 2)),
+    (ALIGN, dict(D=68)), (OK, dict(S=0, q=None)), (OK, dict(T=0, q=None)),
+    (CUDA, dict()), (CUDA, dict(lse=None)),
+])
+def test_prompt_refusals(want, kw):
+    assert _call("pa_prompt_attention", PROMPT_ORDER, PROMPT_BASE, **kw) == want
