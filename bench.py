@@ -881,10 +881,11 @@ def recorded_traffic(config: str, kernel: str, context_tokens: int):
 
 # sources off the 16-bit decode path whose traffic profiles/traffic.json
 # records: the chunked-prefill kernel, its tensor-core helpers, the
-# shared-prefix kernel, the fp8 page steps, the eviction kernels the decode
-# that adds up attention weights and the whole-prompt attention
+# shared-prefix kernel, the fp8 page steps, the eviction kernels, the
+# decode that adds up attention weights and the whole-prompt kernels
 OFF_DECODE_PATH = ("pa_prefill.cuh", "pa_umma.cuh", "pa_shared_prefix.cuh", "pa_decode_fp8.cuh",
-                   "pa_evict.cuh", "pa_decode_weights.cuh", "pa_prompt.cuh")
+                   "pa_evict.cuh", "pa_decode_weights.cuh", "pa_prompt.cuh",
+                   "pa_prompt_weights.cuh")
 
 
 def kernel_source_digest(csrc: Path | None = None) -> str:

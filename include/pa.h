@@ -370,6 +370,26 @@ pa_status pa_prompt_attention(void *out, float *lse, const void *query, const vo
                               void *stream);
 
 /*
+ * pa_prompt_weights -- the attention weight each token of a packed prompt
+ * receives from the last `window` tokens of its sequence (window >= 1; all of
+ * them where the sequence is no longer than that), against the log-sum-exp that
+ * pa_prompt_attention wrote for the same rows:
+ *   weights    [num_seqs, num_kv_heads, max_tokens] fp32 (written): for token j of
+ *              sequence s and KV head kv, the sum over those query tokens i >= j
+ *              and the query heads h of kv of exp(scale * q[i,h].k[j] - lse[i,h])
+ * Entries at or behind a sequence's length stay as they are.  Sums are fp32, in a
+ * fixed order.  A sequence longer than max_tokens is left out and reported
+ * (PA_CHECK_CONTEXT_LEN, index = s), as are bad bounds (PA_CHECK_QUERY).  Other
+ * arguments and limits as pa_prompt_attention.
+ */
+pa_status pa_prompt_weights(float *weights, const void *query, const void *key,
+                            const float *lse, int64_t query_stride, int64_t key_stride,
+                            const int32_t *seq_starts, float scale, int64_t num_seqs,
+                            int64_t num_tokens, int64_t num_heads, int64_t num_kv_heads,
+                            int64_t head_dim, int64_t max_tokens, int64_t window,
+                            pa_dtype dtype, void *stream);
+
+/*
  * pa_decode_weights -- pa_decode that also adds up what each cached token
  * receives, the score that pa_evict_select keeps tokens by.
  *   weights    [num_seqs, num_kv_heads, max_tokens] fp32 (updated): for every

@@ -72,6 +72,7 @@ SIGNATURES = {
     "pa_decode_step_host": (_i, [_p] * 10 + [_i64, _f] + [_i64] * 8 + [_i, _p]),
     "pa_prefill": (_i, [_p] * 7 + [_f] + [_i64] * 9 + [_i, _p]),
     "pa_prompt_attention": (_i, [_p] * 5 + [_i64] * 3 + [_p, _f] + [_i64] * 5 + [_i, _p]),
+    "pa_prompt_weights": (_i, [_p] * 4 + [_i64] * 2 + [_p, _f] + [_i64] * 7 + [_i, _p]),
     "pa_decode_weights_workspace_bytes": (_i64, [_i64] * 5),
     "pa_decode_weights": (_i, [_p] * 3 + [_i64] + [_p] * 5 + [_f] + [_i64] * 9 + [_i, _p]),
     "pa_evict_select": (_i, [_p] * 7 + [_i64] * 6 + [_p]),
@@ -419,6 +420,34 @@ def pa_prompt_attention(out: torch.Tensor, lse: torch.Tensor | None, query: torc
                                     seq_starts.data_ptr(), float(scale), seq_starts.shape[0] - 1,
                                     T, H, Hk, D, dt, _stream(stream))
     _check(st, "pa_prompt_attention")
+
+
+def pa_prompt_weights(weights: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                      lse: torch.Tensor, seq_starts: torch.Tensor, scale: float, window: int,
+                      stream=None) -> None:
+    """The attention weight each token of a packed prompt receives from the last
+    `window` tokens of its sequence, into weights [S, Hk, max_tokens] float32;
+    query, key, seq_starts and scale as pa_prompt_attention, lse as it wrote it."""
+    T, H, D = query.shape
+    Hk = key.shape[1]
+    strides = [_prompt_rows(n, t, T, D) for n, t in (("query", query), ("key", key))]
+    _need(query.dtype == key.dtype, "dtype mismatch")
+    _need(lse.dtype == torch.float32 and lse.shape == (T, H) and lse.is_contiguous(),
+          "lse must be [num_tokens, num_heads] float32")
+    _need(seq_starts.dtype == torch.int32 and seq_starts.dim() == 1 and
+          seq_starts.shape[0] >= 1 and seq_starts.is_contiguous(),
+          "seq_starts must be [num_seqs + 1] int32")
+    S = seq_starts.shape[0] - 1
+    _need(weights.dtype == torch.float32 and weights.dim() == 3 and
+          weights.shape[:2] == (S, Hk) and weights.is_contiguous(),
+          "weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
+    dt = _dtype_code(query)
+    _on_one_device(stream, query, key, lse, weights, seq_starts)
+    st = load().pa_prompt_weights(weights.data_ptr(), query.data_ptr(), key.data_ptr(),
+                                  lse.data_ptr(), *strides, seq_starts.data_ptr(), float(scale),
+                                  S, T, H, Hk, D, weights.shape[2], int(window), dt,
+                                  _stream(stream))
+    _check(st, "pa_prompt_weights")
 
 
 def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, workspace, query: torch.Tensor,

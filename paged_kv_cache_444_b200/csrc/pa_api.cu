@@ -1546,3 +1546,69 @@ extern "C" pa_status pa_prompt_attention(void* out, float* lse, const void* quer
               : launch_prompt_t<128, false>(qm, km, vm, a, items, s);
 }
 // <<< whole-prompt attention
+
+// >>> attention weights of a prompt (pa_prompt_weights): host side.
+#include "pa_prompt_weights.cuh"
+
+namespace {
+template <int D, bool BF16>
+pa_status launch_prompt_weights_t(const CUtensorMap& qm, const CUtensorMap& km,
+                                  const PromptWeightsArgs& a, long long items,
+                                  cudaStream_t stream) {
+  using L = PwSmem<D>;
+  auto kernel = prompt_weights_kernel<D, BF16>;
+  static std::atomic<uint64_t> done{0};
+  if (!ensure_smem(kernel, L::kAlloc, &done)) return PA_ERR_CUDA;
+  const long long sms = sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  return launch_ex(kernel, static_cast<unsigned>(items < sms ? items : sms), kPwThreads, L::kAlloc,
+                   stream, 1, qm, km, a);
+}
+}  // namespace
+
+extern "C" pa_status pa_prompt_weights(float* weights, const void* query, const void* key,
+                                       const float* lse, int64_t query_stride, int64_t key_stride,
+                                       const int32_t* seq_starts, float scale, int64_t num_seqs,
+                                       int64_t num_tokens, int64_t num_heads,
+                                       int64_t num_kv_heads, int64_t head_dim, int64_t max_tokens,
+                                       int64_t window, pa_dtype dtype, void* stream) {
+  pa_status st = check_prompt_sizes(scale, num_seqs, num_tokens, num_heads, num_kv_heads, head_dim,
+                                    dtype);
+  if (st != PA_OK) return st;
+  if (max_tokens <= 0 || max_tokens > INT32_MAX || window <= 0) return PA_ERR_SHAPE;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!weights || !lse || !seq_starts) return PA_ERR_NULL;
+  if ((st = check_prompt_rows(query, query_stride, num_heads * head_dim)) != PA_OK) return st;
+  if ((st = check_prompt_rows(key, key_stride, num_kv_heads * head_dim)) != PA_OK) return st;
+  for (const void* p : {static_cast<const void*>(weights), static_cast<const void*>(lse),
+                        static_cast<const void*>(seq_starts)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return PA_ERR_ALIGN;
+  const int64_t G = num_heads / num_kv_heads, tile = kPrefillRows / G;
+  const long long items = (num_tokens / kPwSpan + num_seqs) * num_kv_heads;   // at most
+  if (items > INT32_MAX) return PA_ERR_SHAPE;
+  CUtensorMap qm, km;
+  if (!encode_rows_map(&qm, query, dtype, num_tokens, num_heads, head_dim, query_stride, G, tile) ||
+      !encode_rows_map(&km, key, dtype, num_tokens, num_kv_heads, head_dim, key_stride, 1, 128))
+    return PA_ERR_CUDA;
+  PromptWeightsArgs a{};
+  a.weights = weights;
+  a.lse = lse;
+  a.seq_starts = seq_starts;
+  a.scale_log2 = scale * kLog2e;
+  a.num_seqs = static_cast<int>(num_seqs);
+  a.num_tokens = static_cast<int>(num_tokens);
+  a.num_heads = static_cast<int>(num_heads);
+  a.num_kv_heads = static_cast<int>(num_kv_heads);
+  a.group = static_cast<int>(G);
+  a.tile_tokens = static_cast<int>(tile);
+  a.max_tokens = static_cast<int>(max_tokens);
+  a.window = static_cast<int>(window < num_tokens ? window : num_tokens);
+  cudaStream_t s = as_stream(stream);
+  const bool bf16 = dtype == PA_BF16;
+  if (head_dim == 64)
+    return bf16 ? launch_prompt_weights_t<64, true>(qm, km, a, items, s)
+                : launch_prompt_weights_t<64, false>(qm, km, a, items, s);
+  return bf16 ? launch_prompt_weights_t<128, true>(qm, km, a, items, s)
+              : launch_prompt_weights_t<128, false>(qm, km, a, items, s);
+}
+// <<< attention weights of a prompt

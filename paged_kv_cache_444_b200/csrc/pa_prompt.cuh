@@ -138,7 +138,8 @@ struct PromptOrder {
 
 // Every thread of the CTA calls it; the same order in every CTA.  A sequence
 // with bad bounds has no units and is reported by one CTA.
-__device__ __forceinline__ PromptOrder prompt_order(const PromptArgs& a, int span, int* sched,
+template <class Args>
+__device__ __forceinline__ PromptOrder prompt_order(const Args& a, int span, int* sched,
                                                     int2* seqs, int* list, int warp, int lane) {
   const int t = threadIdx.x, n = static_cast<int>(blockDim.x);
   const bool table = a.num_seqs <= kPromptRankSeqs;
@@ -197,6 +198,36 @@ __device__ __forceinline__ PromptOrder prompt_order(const PromptArgs& a, int spa
   return o;
 }
 
+// Unit u as (sequence, pair).
+template <class Args>
+__device__ __forceinline__ int2 prompt_unit(const Args& a, const PromptOrder& o, const int2* seqs,
+                                            const int* list, int u, int span) {
+  if (o.ranked) return make_int2(list[u] & 0xffff, list[u] >> 16);
+  if (a.num_seqs <= kPromptRankSeqs) {
+    int lo = 0, hi = a.num_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seqs[mid].y <= u) lo = mid;
+      else hi = mid;
+    }
+    return make_int2(lo, u - seqs[lo].y);
+  }
+  const int n = static_cast<int>(blockDim.x), chunk = (a.num_seqs + n - 1) / n;
+  int lo = 0, hi = n;                  // the last chunk whose first unit is <= u
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  int first = list[lo], s = lo * chunk;
+  for (;; ++s) {                       // u is below the unit count: found before the chunk ends
+    const int units = (max(prompt_len(a.seq_starts, s, a.num_tokens), 0) + span - 1) / span;
+    if (u < first + units || s + 1 >= a.num_seqs) break;
+    first += units;
+  }
+  return make_int2(s, u - first);
+}
+
 struct PromptItem {
   int s, kvh, q0, len, tile_a, lim[2], nkb[2];   // keys each tile's last token sees, their blocks
 };
@@ -206,36 +237,9 @@ __device__ __forceinline__ void prompt_item(const PromptArgs& a, const PromptOrd
                                             PromptItem& it) {
   const int u = i / a.num_kv_heads;
   it.kvh = i - u * a.num_kv_heads;
-  int p;
-  if (o.ranked) {
-    it.s = list[u] & 0xffff;
-    p = list[u] >> 16;
-  } else if (a.num_seqs <= kPromptRankSeqs) {
-    int lo = 0, hi = a.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (seqs[mid].y <= u) lo = mid;
-      else hi = mid;
-    }
-    it.s = lo;
-    p = u - seqs[lo].y;
-  } else {
-    const int n = static_cast<int>(blockDim.x), chunk = (a.num_seqs + n - 1) / n;
-    int lo = 0, hi = n;                // the last chunk whose first unit is <= u
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (list[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    int first = list[lo];
-    it.s = lo * chunk;
-    for (;; ++it.s) {                  // u is below the unit count: found before the chunk ends
-      const int units = (max(prompt_len(a.seq_starts, it.s, a.num_tokens), 0) + span - 1) / span;
-      if (u < first + units || it.s + 1 >= a.num_seqs) break;
-      first += units;
-    }
-    p = u - first;
-  }
+  const int2 unit = prompt_unit(a, o, seqs, list, u, span);
+  const int p = unit.y;
+  it.s = unit.x;
   it.q0 = a.seq_starts[it.s];
   it.len = a.seq_starts[it.s + 1] - it.q0;
   it.tile_a = p * span;

@@ -1,0 +1,369 @@
+// pa_prompt_weights.cuh -- the attention weight each token of a packed prompt
+// receives from the last `window` tokens of its sequence:
+//   weights_j = sum over those query tokens i >= j and the G heads g of
+//               exp(scale q_gi . k_j - lse_gi),
+// given the attention's own log-sum-exp.  No softmax is redone: one product, one
+// 2^x and one addition an element.
+//
+// The products run transposed on the tensor cores, S^T = K Q^T: 128 keys as the
+// MMA's rows, the query rows of a tile (128 / G tokens x G heads, token-major)
+// as its columns.  A thread then owns a key (its tensor-memory lane) and sums
+// over its columns in registers; nothing is shuffled, no sum leaves the thread
+// before it is written, and the order of the additions is fixed.
+//
+// Work item: (sequence, KV head, two blocks of 128 keys).  The item's K stays in
+// shared memory while the query tiles stream through a ring, each loaded once
+// for both key blocks.  One consumer warpgroup a key block, two S^T buffers
+// each, so that the next tile's product runs during this one's 2^x.  Warps: 0-3
+// and 4-7 the key blocks, 8 issues the MMAs, 9 the loads, 10 brings each tile's
+// lse into shared memory (negated, in log2 units).
+#pragma once
+
+#include "pa_prompt.cuh"
+
+namespace pa {
+
+constexpr int kPwThreads = 11 * 32;
+constexpr int kPwSpan = 256;       // keys of an item
+
+struct PromptWeightsArgs {
+  float* weights;              // [S, Hk, max_tokens]
+  const float* lse;            // [T, H]
+  const int32_t* seq_starts;   // [S + 1]
+  float scale_log2;
+  int num_seqs;
+  int num_tokens;
+  int num_heads;
+  int num_kv_heads;
+  int group;
+  int tile_tokens;
+  int max_tokens;
+  int window;
+};
+
+template <int D>
+struct PwSmem {
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kSlab = 128 * 128;
+  static constexpr int kTile = kSlabs * kSlab;        // one key block, or one query tile
+  static constexpr int NK = 2;                        // items' K in flight
+  static constexpr int NQ = D == 64 ? 4 : 2;          // query tiles in flight
+  static constexpr int NL = 4;                        // tiles' lse in flight
+  static constexpr int kK = 0;
+  static constexpr int kQ = kK + NK * 2 * kTile;
+  static constexpr int kLse = kQ + NQ * kTile;        // NL x 128 floats
+  static constexpr int kBarKFull = kLse + NL * 512;
+  static constexpr int kBarKEmpty = kBarKFull + 8 * NK;
+  static constexpr int kBarQFull = kBarKEmpty + 8 * NK;
+  static constexpr int kBarQEmpty = kBarQFull + 8 * NQ;
+  static constexpr int kBarLFull = kBarQEmpty + 8 * NQ;
+  static constexpr int kBarLEmpty = kBarLFull + 8 * NL;
+  static constexpr int kBarSFull = kBarLEmpty + 8 * NL;   // [block][buffer]
+  static constexpr int kBarSEmpty = kBarSFull + 8 * 4;
+  static constexpr int kBarEnd = kBarSEmpty + 8 * 4;
+  static constexpr int kTmemSlot = kBarEnd + 8;
+  static constexpr int kAbort = kTmemSlot + 4;
+  static constexpr int kSched = kAbort + 4;
+  static constexpr int kSeqs = (kSched + 128 + 15) & ~15;
+  static constexpr int kList = kSeqs + 8 * kPromptRankSeqs;
+  static constexpr int kBytes = kList + 4 * kPromptRankUnits;
+  static constexpr int kAlloc = kBytes + 1024;        // one CTA per SM: both sizes pass 114 KB
+  static_assert(kBytes > 114 * 1024, "one CTA holds all of an SM's tensor memory");
+};
+
+struct PwItem {
+  int s, kvh, q0, len;   // sequence, KV head, its first row and its length
+  int k0;                // first key
+  int t0, tiles;         // first query token and the number of query tiles
+  bool two;              // a second key block
+};
+
+// The pairs of a sequence are ranked as the attention's are (more keys, more
+// work); here the first keys are seen by most tokens.
+__device__ __forceinline__ void pw_item(const PromptWeightsArgs& a, const PromptOrder& o,
+                                        const int2* seqs, const int* list, int i, PwItem& it) {
+  const int u = i / a.num_kv_heads;
+  it.kvh = i - u * a.num_kv_heads;
+  const int2 unit = prompt_unit(a, o, seqs, list, u, kPwSpan);
+  it.s = unit.x;
+  it.q0 = a.seq_starts[it.s];
+  it.len = a.seq_starts[it.s + 1] - it.q0;
+  it.k0 = ((it.len + kPwSpan - 1) / kPwSpan - 1 - unit.y) * kPwSpan;
+  it.t0 = max(it.k0, it.len - a.window);
+  it.tiles = (it.len - it.t0 + a.tile_tokens - 1) / a.tile_tokens;
+  it.two = it.k0 + 128 < it.len;
+}
+
+// Whether tile i's tokens see any key of block b.
+__device__ __forceinline__ bool pw_sees(const PwItem& it, int tile_tokens, int i, int b) {
+  return b == 0 || (it.two && min(it.t0 + (i + 1) * tile_tokens, it.len) > it.k0 + 128);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPwThreads, 1)
+    prompt_weights_kernel(const __grid_constant__ CUtensorMap qmap,
+                          const __grid_constant__ CUtensorMap kmap, const PromptWeightsArgs a) {
+  using L = PwSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kWarpTma && lane == 0) {
+    prefetch_tensormap(&qmap);
+    prefetch_tensormap(&kmap);
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int G = a.group;
+  int2* seqs = reinterpret_cast<int2*>(smem + L::kSeqs);
+  int* list = reinterpret_cast<int*>(smem + L::kList);
+  const PromptOrder order = prompt_order(a, kPwSpan, reinterpret_cast<int*>(smem + L::kSched),
+                                         seqs, list, warp, lane);
+  const int total = order.total * a.num_kv_heads;
+  if (prefill_item_index(0, total, blockIdx.x, gridDim.x) < 0) return;
+  const int q_rows = a.tile_tokens * G;
+  float* lse_sh = reinterpret_cast<float*>(smem + L::kLse);
+
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NK; ++i) {
+      mbar_init(sb + L::kBarKFull + 8 * i, 1);
+      mbar_init(sb + L::kBarKEmpty + 8 * i, 1);
+    }
+    for (int i = 0; i < L::NQ; ++i) {
+      mbar_init(sb + L::kBarQFull + 8 * i, 1);
+      mbar_init(sb + L::kBarQEmpty + 8 * i, 1);
+    }
+    for (int i = 0; i < L::NL; ++i) {
+      mbar_init(sb + L::kBarLFull + 8 * i, 32);
+      mbar_init(sb + L::kBarLEmpty + 8 * i, 256);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(sb + L::kBarSFull + 8 * i, 1);
+      mbar_init(sb + L::kBarSEmpty + 8 * i, 128);
+    }
+    mbar_init(sb + L::kBarEnd, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(sb + L::kTmemSlot, kTmemCols);
+  if (warp < 8 && q_rows < 128) {   // rows no query box covers: finite (their lse is +inf)
+    const int chunks = (128 - q_rows) * 8;
+    for (int i = threadIdx.x; i < chunks * L::kSlabs * L::NQ; i += 256) {
+      const int b = i / chunks, c = i % chunks;
+      sts128(sb + L::kQ + b * L::kSlab + q_rows * 128 + c * 16, 0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag)) != 0;
+  };
+
+  if (warp == kWarpTma) {
+    // ================= loads =================
+    int nk = 0, nq = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      if (i < 0) break;
+      PwItem it;
+      pw_item(a, order, seqs, list, i, it);
+      const int ks = nk % L::NK;
+      if (nk >= L::NK && !(ok = wait(sb + L::kBarKEmpty + 8 * ks, ((nk / L::NK) & 1) ^ 1))) break;
+      if (lane == 0) {
+        const int blocks = it.two ? 2 : 1;
+        mbar_arrive_expect_tx(sb + L::kBarKFull + 8 * ks, blocks * L::kTile);
+        for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+          for (int c = 0; c < L::kSlabs; ++c)
+            tma_load_4d(sb + L::kK + (ks * 2 + b) * L::kTile + c * L::kSlab, &kmap,
+                        sb + L::kBarKFull + 8 * ks, 0, c, it.kvh, it.q0 + it.k0 + 128 * b);
+        }
+      }
+      __syncwarp();
+      ++nk;
+      for (int j = 0; j < it.tiles; ++j) {
+        const int qs = nq % L::NQ;
+        if (nq >= L::NQ && !(ok = wait(sb + L::kBarQEmpty + 8 * qs, ((nq / L::NQ) & 1) ^ 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(sb + L::kBarQFull + 8 * qs, L::kSlabs * q_rows * 128);
+#pragma unroll
+          for (int c = 0; c < L::kSlabs; ++c)
+            tma_load_4d(sb + L::kQ + qs * L::kTile + c * L::kSlab, &qmap,
+                        sb + L::kBarQFull + 8 * qs, 0, c, it.kvh * G,
+                        it.q0 + it.t0 + j * a.tile_tokens);
+        }
+        __syncwarp();
+        ++nq;
+      }
+    }
+    // every load issued lands before the CTA can exit
+    for (int g = max(0, nk - L::NK); g < nk; ++g)
+      mbar_wait_bounded(sb + L::kBarKFull + 8 * (g % L::NK), (g / L::NK) & 1);
+    for (int g = max(0, nq - L::NQ); g < nq; ++g)
+      mbar_wait_bounded(sb + L::kBarQFull + 8 * (g % L::NQ), (g / L::NQ) & 1);
+  } else if (warp == kWarpMma) {
+    // ================= MMA issuer =================
+    constexpr uint32_t kId = umma_idesc_f16(BF16, 128, 128, false);
+    int nk = 0, nq = 0, ns[2] = {0, 0};
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      if (i < 0) break;
+      PwItem it;
+      pw_item(a, order, seqs, list, i, it);
+      const int ks = nk % L::NK;
+      if (!(ok = wait(sb + L::kBarKFull + 8 * ks, (nk / L::NK) & 1))) break;
+      for (int j = 0; j < it.tiles && ok; ++j, ++nq) {
+        const int qs = nq % L::NQ;
+        if (!(ok = wait(sb + L::kBarQFull + 8 * qs, (nq / L::NQ) & 1))) break;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (!pw_sees(it, a.tile_tokens, j, b)) continue;
+          const int buf = ns[b] & 1;
+          const uint32_t bar = 8 * (2 * b + buf);
+          if (ns[b] >= 2 && !(ok = wait(sb + L::kBarSEmpty + bar, ((ns[b] >> 1) & 1) ^ 1))) break;
+          tmem_fence_after_sync();
+          if (lane == 0) {
+            const uint32_t kt = sb + L::kK + (ks * 2 + b) * L::kTile, qt = sb + L::kQ + qs * L::kTile;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * L::kSlab + (kk & 3) * 32;
+              umma_f16_ss(tmem + 128 * (2 * b + buf), umma_desc_sw128(kt + off, 16, 1024),
+                          umma_desc_sw128(qt + off, 16, 1024), kId, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(sb + L::kBarSFull + bar);
+          }
+          __syncwarp();
+          ++ns[b];
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          umma_commit(sb + L::kBarQEmpty + 8 * qs);
+          if (j == it.tiles - 1) umma_commit(sb + L::kBarKEmpty + 8 * ks);
+        }
+        __syncwarp();
+      }
+      ++nk;
+    }
+    if (lane == 0) umma_commit(sb + L::kBarEnd);
+    __syncwarp();
+    if (!mbar_wait_bounded(sb + L::kBarEnd, 0) && lane == 0)
+      record_error(kErrWaitTimeout, blockIdx.x);
+  } else if (warp == 10) {
+    // ================= the tiles' lse =================
+    int n = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      if (i < 0) break;
+      PwItem it;
+      pw_item(a, order, seqs, list, i, it);
+      for (int j = 0; j < it.tiles; ++j, ++n) {
+        const int sl = n % L::NL;
+        const int tok0 = it.t0 + j * a.tile_tokens;
+        const int rows = min(a.tile_tokens, it.len - tok0) * G;
+        float v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = lane + 32 * u;
+          v[u] = r < rows ? a.lse[static_cast<size_t>(it.q0 + tok0 + r / G) * a.num_heads +
+                                  it.kvh * G + r % G]
+                          : INFINITY;
+        }
+        if (n >= L::NL && !(ok = wait(sb + L::kBarLEmpty + 8 * sl, ((n / L::NL) & 1) ^ 1))) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)   // a row without a finite logit gives nothing
+          lse_sh[sl * 128 + lane + 32 * u] = v[u] == -INFINITY ? -INFINITY : -v[u] * kLog2e;
+        mbar_arrive(sb + L::kBarLFull + 8 * sl);
+      }
+    }
+  } else {
+    // ================= key block b = warp / 4, key = tensor-memory lane =================
+    const int b = warp >> 2, key = threadIdx.x & 127;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const float2 scale = make_float2(a.scale_log2, a.scale_log2);
+    const float2 one = make_float2(1.f, 1.f);
+    int n = 0, ns = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      if (i < 0) break;
+      PwItem it;
+      pw_item(a, order, seqs, list, i, it);
+      const int kb = it.k0 + 128 * b, kj = kb + key;
+      float acc = 0.f;
+      for (int j = 0; j < it.tiles; ++j, ++n) {
+        const int sl = n % L::NL;
+        if (!(ok = wait(sb + L::kBarLFull + 8 * sl, (n / L::NL) & 1))) break;
+        if (pw_sees(it, a.tile_tokens, j, b)) {
+          const int buf = ns & 1;
+          const uint32_t bar = 8 * (2 * b + buf);
+          if (!(ok = wait(sb + L::kBarSFull + bar, (ns >> 1) & 1))) break;
+          tmem_fence_after_sync();
+          const int tok0 = it.t0 + j * a.tile_tokens;
+          const int rows = min(a.tile_tokens, it.len - tok0) * G;
+          // columns of tokens before this key, or past the tile's rows, do not count
+          const int c0 = max(0, kj - tok0) * G;
+          const bool masked = rows < 128 || tok0 < kb + 127;
+          const float4* lse4 = reinterpret_cast<const float4*>(lse_sh + sl * 128);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float s[32];
+            tmem_ld32(t_lane + 128 * (2 * b + buf) + 32 * h, s);
+            if (masked) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) {
+                const int c = 32 * h + q;
+                s[q] = c >= c0 && c < rows ? s[q] : 0.f;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 neg = lse4[8 * h + q];
+              float2 x = ffma2(make_float2(s[4 * q], s[4 * q + 1]), scale, make_float2(neg.x, neg.y));
+              float2 y = ffma2(make_float2(s[4 * q + 2], s[4 * q + 3]), scale, make_float2(neg.z, neg.w));
+              float2 e = make_float2(ex2(x.x), ex2(x.y)), f = make_float2(ex2(y.x), ex2(y.y));
+              if (masked) {
+                const int c = 32 * h + 4 * q;
+                e.x = c >= c0 ? e.x : 0.f;
+                e.y = c + 1 >= c0 ? e.y : 0.f;
+                f.x = c + 2 >= c0 ? f.x : 0.f;
+                f.y = c + 3 >= c0 ? f.y : 0.f;
+              }
+              sum[0] = ffma2(e, one, sum[0]);
+              sum[1] = ffma2(f, one, sum[1]);
+            }
+          }
+          tmem_fence_before_sync();
+          mbar_arrive(sb + L::kBarSEmpty + bar);
+          acc += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          ++ns;
+        }
+        mbar_arrive(sb + L::kBarLEmpty + 8 * sl);
+      }
+      if (!ok) break;
+      if (it.len > a.max_tokens) {
+        if (key == 0 && b == 0 && it.k0 == 0 && it.kvh == 0) record_error(kErrContextLen, it.s);
+      } else if (kj < it.len) {
+        a.weights[(static_cast<size_t>(it.s) * a.num_kv_heads + it.kvh) * a.max_tokens + kj] = acc;
+      }
+    }
+  }
+
+  tmem_fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tmem_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace pa

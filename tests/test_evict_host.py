@@ -122,3 +122,20 @@ PROMPT_BASE = dict({k: FAKE for k in ("out", "lse", "q", "k", "v", "starts")}, q
 ])
 def test_prompt_refusals(want, kw):
     assert _call("pa_prompt_attention", PROMPT_ORDER, PROMPT_BASE, **kw) == want
+
+
+PW_ORDER = "weights q k lse qs ks starts scale S T H Hk D W window dt".split()
+PW_BASE = dict({k: FAKE for k in ("weights", "q", "k", "lse", "starts")}, qs=1024, ks=256,
+               scale=0.1, S=3, T=100, H=8, Hk=2, D=128, W=50, window=8, dt=1)
+
+
+@host_only
+@pytest.mark.parametrize("want,kw", [
+    (DTYPE, dict(dt=2)), (SHAPE, dict(S=-1)), (SHAPE, dict(window=0)), (SHAPE, dict(W=0)),
+    (SHAPE, dict(ks=128)), (UNSUP, dict(H=64, Hk=2)), (NULL, dict(lse=None)),
+    (NULL, dict(weights=None)), (NULL, dict(q=None)), (ALIGN, dict(qs=1028)),
+    (ALIGN, dict(lse=FAKE + 1)), (ALIGN, dict(k=FAKE + 4)), (OK, dict(S=0)), (OK, dict(T=0)),
+    (CUDA, dict()), (CUDA, dict(window=1 << 40)),
+])
+def test_prompt_weights_refusals(want, kw):
+    assert _call("pa_prompt_weights", PW_ORDER, PW_BASE, **kw) == want
