@@ -156,11 +156,13 @@ def _need(cond: bool, msg: str) -> None:
 def _on_one_device(stream, *tensors) -> None:
     """The library launches on the current device: every tensor must be there
     (and the stream, when it is a torch stream)."""
-    dev = tensors[0].device
-    _need(dev.type == "cuda" and all(t.device == dev for t in tensors),
-          "tensors must be on one CUDA device")
-    _need(dev.index == torch.cuda.current_device(), "tensors must be on the current device")
-    _need(getattr(stream, "device", dev) == dev, "stream and tensors must be on one device")
+    dev = tensors[0].get_device()       # -1: host memory
+    for t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError("tensors must be on one CUDA device")
+    _need(dev == torch.cuda.current_device(), "tensors must be on the current device")
+    if stream is not None and hasattr(stream, "device"):
+        _need(stream.device.index == dev, "stream and tensors must be on one device")
 
 
 # ---------------------------------------------------------------------------

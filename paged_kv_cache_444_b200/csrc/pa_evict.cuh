@@ -48,36 +48,50 @@ __device__ __forceinline__ long long slot_position(const int32_t* positions, int
 // equal to it, the lowest slots that fill the budget.
 //
 // One cluster of C CTAs takes a (sequence, KV head), each CTA a run of its
-// slots, whose keys stay in shared memory between the digit passes (a run too
-// long for it is read again from global memory).  The CTAs add up their
-// histograms through distributed shared memory, and every one finds the same
-// digit.  The kept flags then become one bit each, a warp's share of the run
-// is counted by popcounts, and an exclusive scan over warps and CTAs gives
+// slots, each warp a share of the run in words of 32 slots.  The row is gone
+// through twice: once for the histogram of the top digit, and once, that digit
+// known, to flag the keys above it (a bit a slot) and to list those that share
+// it, few as a rule, from which the other two digits follow.  (A warp with more of
+// them than its list holds goes through its words again instead; up to 8 words a
+// warp stay in registers.)  The CTAs add up their histograms through
+// distributed shared memory, and every one finds the same digit.  Then a thread
+// takes whole words: an exclusive scan of popcounts over threads and CTAs gives
 // every hole and every kept token behind the new length its rank.  The latter
 // leave their slot numbers at their rank in a list spread over the cluster's
-// shared memory (over the keys, which are done with), where the holes fetch
-// theirs.
+// shared memory, where the holes fetch theirs.
+//
+// What bounds it is instructions and the barriers between the steps, not bytes
+// (4 a slot).  8 x 8 rows of 32768 to 131072 slots: 35 us; 105 us when every key
+// was built again for each digit and ranked a slot at a time (315 instructions
+// a word).  128 x 8 rows of 1017 slots: 14.7 us with 128 threads and the keys in
+// registers, 31 us with 512.  A CTA's steps on the long rows, in cycles: top
+// digit 7.2 k and its exchange 5.8 k, flags and lists 9.7 k, the other digits
+// 8 k, ranks and list 10 k.
 // ---------------------------------------------------------------------------
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kDigitBits = 11;
-constexpr int kBins = 1 << kDigitBits;
+constexpr int kBins = 1 << 11;
 
+template <int kThreadsN, bool kReg>
 struct SelectSmem {
-  // [bins] [bins summed over the cluster] [scan sums] [3 counts a warp] [totals] [flags] [keys]
+  static constexpr int kWarpsN = kThreadsN / 32;
+  static constexpr int kListed = kReg ? 0 : 256;   // keys of T's first digit a warp lists
+  // [three histograms] [candidates: key, slot] [2 sums a warp] [totals] [pick]
+  // [flag words] [equal words] [list of moved slots]
   static constexpr int kHist = 0;
-  static constexpr int kSum = kHist + kBins * 4;
-  static constexpr int kScan = kSum + kBins * 4;
-  static constexpr int kWarpCount = kScan + 2 * kSelectWarps * 4;
-  static constexpr int kTotals = kWarpCount + 3 * kSelectWarps * 4;
+  static constexpr int kCand = kHist + 3 * kBins * 4;
+  static constexpr int kScan = kCand + kWarpsN * kListed * 8;
+  static constexpr int kTotals = kScan + 2 * kWarpsN * 4;
   static constexpr int kPick = kTotals + 4 * 4;
-  static constexpr int kFlags = kPick + 4 * 4;   // then flag words, then keys (or the list)
+  static constexpr int kFlags = kPick + 3 * 16;
+  // bytes for a run of `run` slots and `list` entries of the list
+  static __host__ __device__ constexpr int bytes(int run, int list) {
+    return kFlags + (run + 31) / 32 * 8 + 4 * list;
+  }
 };
 
 __device__ __forceinline__ uint32_t claim_key(float w) {
-  if (w != w) return 0u;
   const uint32_t b = __float_as_uint(w + 0.f);    // -0 + 0 = +0
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return w != w ? 0u : k;
 }
 
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
@@ -88,28 +102,33 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-
-// Bytes of shared memory for a run of `run` slots: flag words, and keys when
-// `cached`, else room for this CTA's share of the list of moved slots.
-__host__ __device__ constexpr int select_smem(int run, bool cached, int list) {
-  return SelectSmem::kFlags + (run + 31) / 32 * 4 + 4 * (cached && run > list ? run : list);
+__device__ __forceinline__ uint4 ld_cluster_u32x4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
-__global__ void __launch_bounds__(kSelectThreads, 1)
-    evict_select_kernel(const EvictArgs a, int max_run, int cached) {
+template <int kThreadsN, bool kReg>
+__global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
+    evict_select_kernel(const EvictArgs a, int max_run, int list_shift) {
+  using L = SelectSmem<kThreadsN, kReg>;
+  constexpr int kWarpsN = L::kWarpsN;
+  constexpr int kBatch = 8;                            // words a warp loads before it uses any
   extern __shared__ __align__(16) uint8_t smem[];
-  uint32_t* hist = reinterpret_cast<uint32_t*>(smem + SelectSmem::kHist);
-  uint32_t* sum = reinterpret_cast<uint32_t*>(smem + SelectSmem::kSum);
-  uint32_t* scan = reinterpret_cast<uint32_t*>(smem + SelectSmem::kScan);
-  uint32_t* wcount = reinterpret_cast<uint32_t*>(smem + SelectSmem::kWarpCount);
-  uint32_t* totals = reinterpret_cast<uint32_t*>(smem + SelectSmem::kTotals);
-  uint32_t* pick = reinterpret_cast<uint32_t*>(smem + SelectSmem::kPick);
-  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + SelectSmem::kFlags);
-  uint32_t* keys = flags + (max_run + 31) / 32;
+  uint2* cand = reinterpret_cast<uint2*>(smem + L::kCand);
+  uint32_t* scan = reinterpret_cast<uint32_t*>(smem + L::kScan);
+  uint32_t* totals = reinterpret_cast<uint32_t*>(smem + L::kTotals);
+  uint4* pick = reinterpret_cast<uint4*>(smem + L::kPick);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + L::kFlags);
+  uint32_t* same = flags + (max_run + 31) / 32;
+  uint32_t* list = same + (max_run + 31) / 32;
   const int C = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int row = blockIdx.x / C;                      // s * Hk + kv
   const int s = row / a.num_kv_heads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int b = tid; b < 3 * kBins / 4; b += kThreadsN)
+    reinterpret_cast<uint4*>(smem + L::kHist)[b] = make_uint4(0, 0, 0, 0);
   pdl_launch_dependents();
   pdl_wait();
 
@@ -124,62 +143,109 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
   if (tid == 0 && rank == 0 && row % a.num_kv_heads == 0) a.new_lens[s] = kept;
   int32_t* source = a.source + static_cast<size_t>(row) * B;
   if (n <= B) {                                        // everything stays
-    for (int i = rank * kSelectThreads + tid; i < B; i += C * kSelectThreads)
-      source[i] = i < n ? i : -1;
+    for (int i = rank * kThreadsN + tid; i < B; i += C * kThreadsN) source[i] = i < n ? i : -1;
     return;
   }
 
-  // ---- this CTA's run of slots, a multiple of 32 ----
+  // ---- this CTA's run of slots, a multiple of 32, and this warp's words of it ----
   const int per = ((n + C - 1) / C + 31) & ~31;        // <= max_run
   const int lo = min(rank * per, n), run = min(per, n - lo);
-  const size_t base = static_cast<size_t>(row) * a.max_tokens;
-  const float* w = a.weights + base;
-  const int32_t* pos = a.positions + base;
-  const int recorded = min(max(a.recorded_lens[s], 0), n);
-  const int len = a.seq_lens[s];
-  const long long first_recent = static_cast<long long>(len) - a.recent;
-  auto make_key = [&](int i) -> uint32_t {             // slot lo + i
-    const long long p = slot_position(pos, recorded, len, n, lo + i);
-    return (p < a.sink || p >= first_recent) ? 0xffffffffu : claim_key(w[lo + i]);
-  };
-  auto key_at = [&](int i) -> uint32_t { return cached ? keys[i] : make_key(i); };
+  const int words = (run + 31) / 32, wper = (words + kWarpsN - 1) / kWarpsN;
+  const int w0 = min(warp * wper, words), w1 = min(w0 + wper, words);
+  const size_t base = static_cast<size_t>(row) * a.max_tokens + lo;
+  const float* __restrict__ w = a.weights + base;
+  const int32_t* __restrict__ pos = a.positions + base;
+  const int recorded = min(max(a.recorded_lens[s], 0), n) - lo;   // relative to the run, too
+  // recorded positions are held below `sink` and from `first_recent` on; the
+  // slots after them, whose positions follow their order, below `held_lo` and
+  // from `held_hi` on
+  auto clamp = [](long long x, int hi) { return static_cast<int>(x < 0 ? 0 : x > hi ? hi : x); };
+  const long long len = a.seq_lens[s];
+  const int first_recent = static_cast<int>(len - a.recent < INT32_MIN ? INT32_MIN : len - a.recent);
+  const long long late = len - n + lo;                 // position of slot i: late + i
+  const int held_lo = clamp(a.sink - late, run), held_hi = clamp(len - a.recent - late, run);
 
-  uint32_t prefix = 0;                                 // digits of T found so far
-  uint32_t need = B;                                   // kept keys among those that share them
-  uint32_t equal = 0;                                  // keys that share them
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bits = pass == 2 ? 10 : 11;
-    for (int b = tid; b < kBins; b += kSelectThreads) hist[b] = 0;
-    __syncthreads();
-    for (int i = tid; i < run; i += kSelectThreads) {
-      uint32_t k;
-      if (pass == 0) {
-        k = make_key(i);
-        if (cached) keys[i] = k;
-      } else {
-        k = key_at(i);
-        if ((k >> (shift + bits)) != prefix) continue;
-      }
-      atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+  // Keys of kBatch words from q of the warp's share (0 past its end); true if
+  // they are whole words of slots that have only their weight.
+  auto load = [&](int q, uint32_t (&k)[kBatch]) -> bool {
+    const int i0 = q * 32 + lane;
+    float x[kBatch];
+    if (q + kBatch <= w1 && q * 32 >= recorded && q * 32 >= held_lo &&
+        (q + kBatch) * 32 <= held_hi) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) x[u] = __ldg(w + i0 + 32 * u);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) k[u] = claim_key(x[u]);
+      return true;
     }
-    __syncthreads();
-    if (C > 1) {
-      cluster_sync();
-      for (int b = tid; b < kBins; b += kSelectThreads) {
-        uint32_t t = 0;
-        for (int c = 0; c < C; ++c) t += ld_cluster_u32(map_cluster(smem_addr(&hist[b]), c));
-        sum[b] = t;
-      }
-      cluster_sync();                                  // hist is cleared for the next digit
+    int p[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + 32 * u;
+      const bool in = q + u < w1 && i < run;
+      x[u] = in ? __ldg(w + i) : 0.f;
+      p[u] = in && i < recorded ? __ldg(pos + i) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + 32 * u;
+      const bool held = i < recorded ? p[u] < a.sink || p[u] >= first_recent
+                                     : i < held_lo || i >= held_hi;
+      k[u] = q + u < w1 && i < run ? (held ? 0xffffffffu : claim_key(x[u])) : 0u;
+    }
+    return false;
+  };
+  uint32_t held_keys[kBatch];
+  if constexpr (kReg) load(w0, held_keys);
+  // f(first word, keys, whether every slot of the words is one of the run)
+  auto each = [&](auto&& f) {
+    if constexpr (kReg) {
+      f(w0, held_keys, false);
     } else {
-      for (int b = tid; b < kBins; b += kSelectThreads) sum[b] = hist[b];
-      __syncthreads();
+      for (int q = w0; q < w1; q += kBatch) {
+        uint32_t k[kBatch];
+        if (load(q, k)) f(q, k, true);
+        else f(q, k, false);
+      }
     }
-    // thread t: bins kBins - 1 - 2t and kBins - 2 - 2t, from the top
-    const uint32_t c0 = sum[kBins - 1 - 2 * tid], c1 = sum[kBins - 2 - 2 * tid];
-    uint32_t incl = c0 + c1;
+  };
+  auto hist_of = [&](int pass) {
+    return reinterpret_cast<uint32_t*>(smem + L::kHist) + pass * kBins;
+  };
+  // the slot of word q in this lane is one of this warp's (a key of 0 past the
+  // end must not count)
+  auto mine = [&](int q) { return q < w1 && q * 32 + lane < run; };
+
+  // The digit of T from the cluster's summed histogram: (bin, how many of its
+  // keys stay, how many there are).
+  uint32_t need = B;
+  auto digit = [&](int pass) -> uint4 {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    constexpr int kQuads = kBins / kThreadsN / 4;      // uint4 of bins a thread
+    const uint32_t* hist = hist_of(pass);
+    const int top = kBins - 4 * kQuads * (tid + 1);    // this thread's bins, from the top
+    uint4 c[kQuads];
+    uint32_t own = 0;
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      c[q] = *reinterpret_cast<const uint4*>(&hist[top + 4 * q]);
+      if (C > 1) {
+        const uint32_t at = smem_addr(&hist[top + 4 * q]);
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+          if (r < C) {
+            const uint4 v = ld_cluster_u32x4(map_cluster(at, (rank + r) % C));
+            c[q].x += v.x;
+            c[q].y += v.y;
+            c[q].z += v.z;
+            c[q].w += v.w;
+          }
+        }
+      }
+      own += (c[q].x + c[q].y) + (c[q].z + c[q].w);
+    }
+    uint32_t incl = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, incl, d);
@@ -187,125 +253,206 @@ __global__ void __launch_bounds__(kSelectThreads, 1)
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    if (warp == 0) {
-      uint32_t x = scan[lane];
+    uint32_t above = incl - own;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += v;
+    for (int v = 0; v < kWarpsN; ++v)
+      if (v < warp) above += scan[v];
+    if (above < need && above + own >= need) {        // one thread
+#pragma unroll
+      for (int q = kQuads - 1; q >= 0; --q) {
+        const uint32_t bins[4] = {c[q].w, c[q].z, c[q].y, c[q].x};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (above < need && above + bins[e] >= need)
+            pick[pass] = make_uint4(top + 4 * q + 3 - e, need - above, bins[e], 0);
+          above += bins[e];
+        }
       }
-      scan[kSelectWarps + lane] = x;
     }
     __syncthreads();
-    const uint32_t above = (warp ? scan[kSelectWarps + warp - 1] : 0) + incl - c0 - c1;
-    if (above < need && above + c0 >= need) {
-      pick[0] = kBins - 1 - 2 * tid;
-      pick[1] = need - above;
-      pick[2] = c0;
-    } else if (above + c0 < need && above + c0 + c1 >= need) {
-      pick[0] = kBins - 2 - 2 * tid;
-      pick[1] = need - above - c0;
-      pick[2] = c1;
-    }
-    __syncthreads();
-    prefix = (prefix << bits) | pick[0];
-    need = pick[1];
-    equal = pick[2];
-    __syncthreads();
-  }
-  const uint32_t T = prefix;
-  const bool cut = equal != need;                      // only some keys equal to T stay
+    return pick[pass];
+  };
 
-  // ---- flags, a warp's share of the run at a time; words of 32 slots ----
-  const int words = (run + 31) / 32, wper = (words + kSelectWarps - 1) / kSelectWarps;
-  const int w0 = min(warp * wper, words), w1 = min(w0 + wper, words);
+  __syncthreads();                                     // the histograms are clear
+  uint32_t* h0 = hist_of(0);
+  each([&](int q, const uint32_t (&k)[kBatch], bool whole) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (whole || mine(q + u)) atomicAdd(&h0[k[u] >> 21], 1u);
+  });
+  const uint4 d0 = digit(0);
+  need = d0.y;
+  uint32_t* h1 = hist_of(1);
+  uint2* wcand = cand + warp * L::kListed;             // this warp's list
+  int listed_keys = 0;
   const uint32_t below = (1u << lane) - 1;
-  // exclusive scan of one count a warp over the cluster's warps, in order of
+  each([&](int q, const uint32_t (&k)[kBatch], bool whole) {
+    uint32_t word = 0;                                 // lane u: the flags of word q + u
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint32_t top = k[u] >> 21;
+      const uint32_t f = __ballot_sync(0xffffffffu, top > d0.x);
+      if (lane == u) word = f;
+      if constexpr (!kReg) {
+        const bool c = top == d0.x && (whole || mine(q + u));
+        const uint32_t m = __ballot_sync(0xffffffffu, c);
+        if (m) {
+          const int at = listed_keys + __popc(m & below);
+          if (c && at < L::kListed) wcand[at] = make_uint2(k[u], (q + u) * 32 + lane);
+          listed_keys += __popc(m);
+        }
+      }
+    }
+    if (lane < kBatch && (whole || q + lane < w1)) {
+      flags[q + lane] = word;
+      same[q + lane] = 0;
+    }
+  });
+  const bool listed = !kReg && listed_keys <= L::kListed;   // else this warp goes through its words again
+  __syncwarp();
+  // f(key, slot) over this warp's keys that share T's first digit
+  auto candidates = [&](auto&& f) {
+    if (listed) {
+      for (int i = lane; i < listed_keys; i += 32) f(wcand[i].x, static_cast<int>(wcand[i].y));
+    } else {
+      each([&](int q, const uint32_t (&k)[kBatch], bool) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if ((k[u] >> 21) == d0.x && mine(q + u)) f(k[u], (q + u) * 32 + lane);
+      });
+    }
+  };
+  candidates([&](uint32_t k, int) { atomicAdd(&h1[(k >> 10) & 2047u], 1u); });
+  const uint4 d1 = digit(1);
+  need = d1.y;
+  uint32_t* h2 = hist_of(2);
+  const uint32_t prefix = d0.x << 11 | d1.x;
+  candidates([&](uint32_t k, int) {
+    if ((k >> 10) == prefix) atomicAdd(&h2[k & 1023u], 1u);
+  });
+  const uint4 d2 = digit(2);
+  need = d2.y;
+  const uint32_t T = prefix << 10 | d2.x;
+  const bool cut = d2.z != need;                       // only some keys equal to T stay
+  candidates([&](uint32_t k, int i) {
+    if (k >= T) atomicOr(cut && k == T ? &same[i >> 5] : &flags[i >> 5], 1u << (i & 31));
+  });
+  __syncthreads();
+
+  // ---- ranks, a thread a share of whole words ----
+  // exclusive scan of a pair of counts over the cluster's threads, in order of
   // the slots; every CTA calls it (it holds cluster barriers)
-  auto before = [&](uint32_t mine, int slot) -> uint32_t {
-    if (lane == 0) wcount[slot * kSelectWarps + warp] = mine;
-    __syncthreads();
-    uint32_t v = wcount[slot * kSelectWarps + lane];
-    const uint32_t own = v;
+  auto before = [&](uint32_t x, uint32_t y, int slot) -> uint2 {
+    uint32_t ix = x, iy = y;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v += u;
+      const uint32_t u = __shfl_up_sync(0xffffffffu, ix, d), v = __shfl_up_sync(0xffffffffu, iy, d);
+      if (lane >= d) {
+        ix += u;
+        iy += v;
+      }
     }
-    const uint32_t total = __shfl_sync(0xffffffffu, v, 31);
-    const uint32_t first = __shfl_sync(0xffffffffu, v - own, warp);
-    if (C == 1) return first;
-    if (tid == 0) totals[slot] = total;
-    cluster_sync();
-    uint32_t ahead = 0;
-    for (int c = 0; c < rank; ++c) ahead += ld_cluster_u32(map_cluster(smem_addr(&totals[slot]), c));
-    return ahead + first;
+    if (lane == 31) {
+      scan[warp] = ix;
+      scan[kWarpsN + warp] = iy;
+    }
+    __syncthreads();
+    ix -= x;
+    iy -= y;
+    uint32_t tx = 0, ty = 0;
+#pragma unroll
+    for (int v = 0; v < kWarpsN; ++v) {
+      if (v == warp) {
+        ix += tx;
+        iy += ty;
+      }
+      tx += scan[v];
+      ty += scan[kWarpsN + v];
+    }
+    if (C > 1) {
+      if (tid == 0) {
+        totals[2 * slot] = tx;
+        totals[2 * slot + 1] = ty;
+      }
+      cluster_sync();
+      for (int c = 0; c < rank; ++c) {
+        ix += ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot]), c));
+        iy += ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot + 1]), c));
+      }
+    } else {
+      __syncthreads();                                 // the sums are used again
+    }
+    return make_uint2(ix, iy);
   };
-  uint32_t ties = 0;
+  const int tper = (words + kThreadsN - 1) / kThreadsN;
+  const int t0 = min(tid * tper, words), t1 = min(t0 + tper, words);
   if (cut) {
-    uint32_t mine = 0;
-    for (int q = w0; q < w1; ++q) {
-      const int i = q * 32 + lane;
-      mine += __popc(__ballot_sync(0xffffffffu, i < run && key_at(i) == T));
+    uint32_t ties = 0;
+    for (int q = t0; q < t1; ++q) ties += __popc(same[q]);
+    ties = before(ties, 0, 0).x;
+    for (int q = t0; q < t1; ++q) {                    // the first `need` of them stay
+      uint32_t e = same[q], take = 0;
+      for (; e && ties < need; ++ties, e &= e - 1) take |= e & (0u - e);
+      ties += __popc(e);
+      flags[q] |= take;
     }
-    ties = before(mine, 0);
   }
   const int front = min(max(kept - lo, 0), run);       // slots of the run below the new length
+  // bits of word q below the new length
+  auto front_bits = [&](int q) -> uint32_t {
+    const int m = front - q * 32;
+    return m >= 32 ? 0xffffffffu : m <= 0 ? 0u : (1u << m) - 1;
+  };
   uint32_t holes = 0, tails = 0;
-  for (int q = w0; q < w1; ++q) {
-    const int i = q * 32 + lane;
-    const uint32_t k = i < run ? key_at(i) : 0u;
-    bool keep = i < run && k >= T;
-    if (cut) {
-      const uint32_t eq = __ballot_sync(0xffffffffu, i < run && k == T);
-      if (keep && k == T) keep = ties + __popc(eq & below) < need;
-      ties += __popc(eq);
-    }
-    const uint32_t f = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) flags[q] = f;
-    const uint32_t in = __ballot_sync(0xffffffffu, i < front);
+  for (int q = t0; q < t1; ++q) {
+    const uint32_t f = flags[q], in = front_bits(q);
     holes += __popc(in & ~f);
     tails += __popc(f & ~in);
   }
-  holes = before(holes, 1);
-  tails = before(tails, 2);                            // (its barrier: every key is done with)
+  const uint2 first = before(holes, tails, 1);
 
-  // ---- the list of moved slots, entry r in CTA r / lper ----
-  const int lper = (min(B, n - B) + C - 1) / C;
-  for (int q = w0; q < w1; ++q) {
-    const int i = q * 32 + lane;
-    const uint32_t f = flags[q];
-    const uint32_t t = f & __ballot_sync(0xffffffffu, i >= front);
-    if ((t >> lane) & 1u) {
-      const int r = tails + __popc(t & below);
-      st_cluster_u32(map_cluster(smem_addr(&keys[r % lper]), r / lper), lo + i);
+  // ---- the list of moved slots, entry r in CTA r >> list_shift ----
+  const uint32_t mask = (1u << list_shift) - 1;
+  const uint32_t list_at = smem_addr(list);
+  uint32_t r = first.y;
+  for (int q = t0; q < t1; ++q) {
+    for (uint32_t t = flags[q] & ~front_bits(q); t; t &= t - 1, ++r) {
+      const uint32_t slot = lo + q * 32 + __ffs(t) - 1;
+      if (C > 1) st_cluster_u32(map_cluster(list_at + 4 * (r & mask), r >> list_shift), slot);
+      else list[r] = slot;
     }
-    tails += __popc(t);
   }
-  cluster_sync();
-  for (int q = w0; q < w1 && q * 32 < front; ++q) {
-    const int i = q * 32 + lane;
-    const uint32_t f = flags[q];
-    const uint32_t h = ~f & __ballot_sync(0xffffffffu, i < front);
-    int from = lo + i;
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+  // a word's holes take consecutive entries: the word's first rank goes where
+  // the word's equal bits were, and a warp then writes whole words
+  r = first.x;
+  for (int q = t0; q < t1; ++q) {
+    same[q] = r;
+    r += __popc(front_bits(q) & ~flags[q]);
+  }
+  __syncthreads();
+  for (int q = warp; q * 32 < front; q += kWarpsN) {
+    const uint32_t h = front_bits(q) & ~flags[q];
+    int from = lo + q * 32 + lane;
     if ((h >> lane) & 1u) {
-      const int r = holes + __popc(h & below);
-      from = ld_cluster_u32(map_cluster(smem_addr(&keys[r % lper]), r / lper));
+      const uint32_t e = same[q] + __popc(h & below);
+      from = C > 1 ? ld_cluster_u32(map_cluster(list_at + 4 * (e & mask), e >> list_shift)) : list[e];
     }
-    holes += __popc(h);
-    if (i < front) source[lo + i] = from;
+    if (q * 32 + lane < front) source[lo + q * 32 + lane] = from;
   }
   if (C > 1) cluster_sync();                           // no CTA leaves while its list is read
 }
 
 // ---------------------------------------------------------------------------
 // Compact: slot i < new_lens[s] takes the row of slot source[i].  A CTA takes
-// kCompactSlots slots of one (sequence, KV head): each thread looks at one and
-// moves its weight and position, the slots to move go into a list, and the CTA
-// copies their K and V rows in 16-byte units, consecutive threads along a row.
+// 256 kPer slots of one (sequence, KV head): each thread looks at kPer of them
+// and moves their weights and positions, the slots to move go into a list, and
+// the CTA copies their K and V rows in 16-byte units, consecutive threads along a
+// row.
 // ---------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;
-constexpr int kCompactSlots = 256;
+constexpr int kCompactBatch = 4;      // units of K and of V a thread loads before it stores any
 
 struct CompactArgs {
   EvictArgs e;
@@ -319,9 +466,10 @@ struct CompactArgs {
   int chunks;                    // CTAs per (sequence, KV head)
 };
 
+template <int kPer>
 __global__ void __launch_bounds__(kCompactThreads)
     evict_compact_kernel(const CompactArgs a) {
-  __shared__ int2 list[kCompactSlots];       // (source, destination) rows of the flat cache
+  __shared__ int2 list[kCompactThreads * kPer];   // (source, destination) rows of the flat cache
   __shared__ int moves;
   const int tid = threadIdx.x;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
@@ -329,15 +477,15 @@ __global__ void __launch_bounds__(kCompactThreads)
   if (tid == 0) moves = 0;
   pdl_launch_dependents();
   pdl_wait();
-  __syncthreads();
   const int n = a.e.context_lens[s], kept = a.e.new_lens[s];
+  const int recorded = min(max(a.e.recorded_lens[s], 0), n);
+  const int len = a.e.seq_lens[s];
   if (n < 0 || n > a.e.max_tokens || kept < 0 || kept > n || kept > a.e.budget) {
     if (tid == 0 && chunk == 0 && kv == 0) record_error(kErrContextLen, s);
     return;
   }
-  const int recorded = min(max(a.e.recorded_lens[s], 0), n);
-  const int len = a.e.seq_lens[s];
   const size_t base = static_cast<size_t>(row) * a.e.max_tokens;
+  const int32_t* source = a.e.source + static_cast<size_t>(row) * a.e.budget;
   const int32_t* table = a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq;
   // flat row of a slot, or -1 (reported) if its block id is out of range
   auto flat = [&](int i) -> int {
@@ -349,20 +497,29 @@ __global__ void __launch_bounds__(kCompactThreads)
     }
     return id * a.block_size + i % a.block_size;
   };
-  const int i = chunk * kCompactSlots + tid;
-  if (i < kept) {
-    const int j = a.e.source[static_cast<size_t>(row) * a.e.budget + i];
+  const int i0 = chunk * kCompactThreads * kPer + tid;
+  int from[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = i0 + u * kCompactThreads;
+    from[u] = i < kept ? __ldg(source + i) : i;
+  }
+  __syncthreads();                                // the count is clear
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = i0 + u * kCompactThreads, j = from[u];
+    if (i >= kept) continue;
     if (j != i && (j < kept || j >= n)) {
       record_error(kErrSource, static_cast<long long>(row) * a.e.budget + i);
-    } else {
-      if (j != i || i >= recorded)
-        a.e.positions[base + i] = static_cast<int32_t>(
-            slot_position(a.e.positions + base, recorded, len, n, j));
-      if (j != i) {
-        a.e.weights[base + i] = a.e.weights[base + j];
-        const int src = flat(j), dst = flat(i);
-        if (src >= 0 && dst >= 0) list[atomicAdd(&moves, 1)] = make_int2(src, dst);
-      }
+      continue;
+    }
+    if (j != i || i >= recorded)
+      a.e.positions[base + i] = static_cast<int32_t>(
+          slot_position(a.e.positions + base, recorded, len, n, j));
+    if (j != i) {
+      a.e.weights[base + i] = a.e.weights[base + j];
+      const int src = flat(j), dst = flat(i);
+      if (src >= 0 && dst >= 0) list[atomicAdd(&moves, 1)] = make_int2(src, dst);
     }
   }
   __syncthreads();
@@ -372,12 +529,27 @@ __global__ void __launch_bounds__(kCompactThreads)
   const uint4* vs = reinterpret_cast<const uint4*>(a.value_cache);
   uint4* kd = reinterpret_cast<uint4*>(a.key_cache);
   uint4* vd = reinterpret_cast<uint4*>(a.value_cache);
-  for (int u = tid; u < units; u += kCompactThreads) {
-    const int m = u / a.row_units, c = u - m * a.row_units + kv * a.row_units;
-    const int2 e = list[m];
-    const uint4 k = ks[e.x * stride + c], v = vs[e.x * stride + c];
-    kd[e.y * stride + c] = k;
-    vd[e.y * stride + c] = v;
+  for (int u0 = tid; u0 < units; u0 += kCompactThreads * kCompactBatch) {
+    uint4 k[kCompactBatch], v[kCompactBatch];
+    size_t to[kCompactBatch];
+#pragma unroll
+    for (int q = 0; q < kCompactBatch; ++q) {
+      const int u = u0 + q * kCompactThreads;
+      if (u < units) {
+        const int m = u / a.row_units, c = u - m * a.row_units + kv * a.row_units;
+        const int2 e = list[m];
+        to[q] = e.y * stride + c;
+        k[q] = ks[e.x * stride + c];
+        v[q] = vs[e.x * stride + c];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kCompactBatch; ++q) {
+      if (u0 + q * kCompactThreads < units) {
+        kd[to[q]] = k[q];
+        vd[to[q]] = v[q];
+      }
+    }
   }
 }
 
