@@ -99,6 +99,22 @@ __device__ __forceinline__ void regs_shrink() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// One lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// x of lane 0: a value that the whole warp shares, known to the compiler as one.
+// The MMA's operands sit in uniform registers; one computed from a value that
+// the compiler takes for a lane's own is moved there for every MMA.
+__device__ __forceinline__ int warp_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Store 32 32-bit columns of this thread's lane (complete after tmem_wait_st).
 __device__ __forceinline__ void tmem_st32u_async(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -329,7 +345,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (warp == kWarpTma && lane == 0) {
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
@@ -453,26 +469,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // ================= MMA issuer =================
       constexpr uint32_t kIdS = umma_idesc_f16(BF16, kPrefillRows, kPrefillKeys, false);
       constexpr uint32_t kIdO = umma_idesc_f16(BF16, kPrefillRows, D, true);
-      auto issue_s = [&](int t, int g) {
-        const uint32_t kst = sb + L::kK + (g % NST) * L::kStage;
-        const uint32_t qt = sb + L::kQ + t * L::kQTile;
+      constexpr uint32_t kStage16 = L::kStage / 16;
+      const uint32_t tm = warp_uniform(tmem);
+      const uint64_t qdesc = umma_desc_sw128(sb + L::kQ, 16, 1024);
+      const uint64_t kdesc = umma_desc_sw128(sb + L::kK, 16, 1024);
+      const uint64_t vdesc = umma_desc_sw128(sb + L::kV, L::kSlab, 1024);
+      const bool leader = elect_lane();
+      auto issue_s = [&](int t, int st) {
+        const uint64_t q = qdesc + t * (L::kQTile / 16), kd = kdesc + st * kStage16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * L::kSlab + (kk & 3) * 32;
-          umma_f16_ss(tmem + kTmemS + 128 * t, umma_desc_sw128(qt + off, 16, 1024),
-                      umma_desc_sw128(kst + off, 16, 1024), kIdS, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) / 16;
+          umma_f16_ss(tm + kTmemS + 128 * t, q + off, kd + off, kIdS, kk > 0 ? 1u : 0u);
         }
         umma_commit(sb + L::kBarS + 8 * t);
       };
-      // O_t (+)= P_t V_g over the 16-key steps below the tile's last key
-      auto issue_pv = [&](int t, int g, int j, int lim) {
-        const uint32_t vst = sb + L::kV + (g % NST) * L::kStage;
-        const uint32_t pcol = tmem + kTmemS + 128 * t;
-        const int steps = min(kPrefillKeys / 16, (lim - j * kPrefillKeys + 15) / 16);
-        for (int k = 0; k < steps; ++k)
-          umma_f16_ts(tmem + kTmemO + 128 * t, pcol + 8 * k,
-                      umma_desc_sw128(vst + k * 2048, L::kSlab, 1024), kIdO,
-                      (j > 0 || k > 0) ? 1u : 0u);
+      // O_t (+)= P_t V over the 16-key steps below the tile's last key (`keys` of the block)
+      auto issue_pv = [&](int t, int st, bool first, int keys) {
+        const uint64_t vd = vdesc + st * kStage16;
+        const uint32_t o = tm + kTmemO + 128 * t, p = tm + kTmemS + 128 * t;
+        if (keys > kPrefillKeys - 16) {
+#pragma unroll
+          for (int k = 0; k < kPrefillKeys / 16; ++k)
+            umma_f16_ts(o, p + 8 * k, vd + k * 128, kIdO, k > 0 || !first ? 1u : 0u);
+        } else {
+          for (int k = 0; k * 16 < keys; ++k)
+            umma_f16_ts(o, p + 8 * k, vd + k * 128, kIdO, k > 0 || !first ? 1u : 0u);
+        }
       };
       auto wait = [&](uint32_t bar, uint32_t parity) {
         const bool r = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
@@ -480,61 +503,71 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         return r;
       };
       // The issue order is S_A(j), P_B(j-1) V, S_B(j), P_A(j) V, so that each
-      // tile's softmax overlaps the other tile's products.  g0: blocks before
-      // this item; done[t], items[t]: S/P rounds and items of tile t.
-      int n_q = 0, g0 = 0, done[2] = {0, 0}, items[2] = {0, 0};
+      // tile's softmax overlaps the other tile's products.  g: blocks so far
+      // (st their stage, par its phase); done[t], items[t]: S/P rounds and items
+      // of tile t.
+      int n_q = 0, st = 0, par = 0, done[2] = {0, 0}, items[2] = {0, 0};
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
         if (i < 0) break;
         PromptItem it;
         prompt_item(a, order, seqs, list, i, span, it);
-        const int nkb = max(it.nkb[0], it.nkb[1]);
-        // P_t of block j is in: its product, after the epilogue has read the last item's O_t
-        auto pv = [&](int t, int j) {
+        const int nkb[2] = {warp_uniform(it.nkb[0]), warp_uniform(it.nkb[1])};
+        const int lim[2] = {warp_uniform(it.lim[0]), warp_uniform(it.lim[1])};
+        const int blocks = max(nkb[0], nkb[1]);
+        // P_t of block j (stage vs, phase vpar) is in: its product, after the
+        // epilogue has read the last item's O_t
+        auto pv = [&](int t, int j, int vs, int vpar) {
           if (j == 0 && items[t] > 0 && !wait(sb + L::kBarOFree + 8 * t, (items[t] - 1) & 1))
             return false;
-          const int g = g0 + j;
-          if (!wait(sb + L::kBarVOk + 8 * (g % NST), (g / NST) & 1) ||
+          if (!wait(sb + L::kBarVOk + 8 * vs, vpar) ||
               !wait(sb + L::kBarP + 8 * t, (done[t] + j) & 1))
             return false;
-          if (lane == 0) issue_pv(t, g, j, it.lim[t]);
+          if (leader) issue_pv(t, vs, j == 0, lim[t] - j * kPrefillKeys);
           __syncwarp();
           return true;
         };
         if (!(ok = wait(sb + L::kBarQ, n_q & 1))) break;
         ++n_q;
-        for (int j = 0; j <= nkb && ok; ++j) {
-          const int g = g0 + j;
-          if (j < nkb && !(ok = wait(sb + L::kBarKFull + 8 * (g % NST), (g / NST) & 1))) break;
-          if (j < it.nkb[0]) {
-            if (lane == 0) issue_s(0, g);
+        int last = 0, lpar = 0;            // the block before: stage and phase
+        for (int j = 0; j <= blocks && ok; ++j) {
+          if (j < blocks && !(ok = wait(sb + L::kBarKFull + 8 * st, par))) break;
+          if (j < nkb[0]) {
+            if (leader) issue_s(0, st);
             __syncwarp();
           }
-          if (j > 0 && j - 1 < it.nkb[1] && !(ok = pv(1, j - 1))) break;
-          if (lane == 0) {
-            if (j > 0) umma_commit(sb + L::kBarVEmpty + 8 * ((g - 1) % NST));
-            if (j < it.nkb[1]) issue_s(1, g);
-            if (j < nkb) umma_commit(sb + L::kBarKEmpty + 8 * (g % NST));
-            if (j == nkb - 1) umma_commit(sb + L::kBarQFree);
+          if (j > 0 && j - 1 < nkb[1] && !(ok = pv(1, j - 1, last, lpar))) break;
+          if (leader) {
+            if (j > 0) umma_commit(sb + L::kBarVEmpty + 8 * last);
+            if (j < nkb[1]) issue_s(1, st);
+            if (j < blocks) umma_commit(sb + L::kBarKEmpty + 8 * st);
+            if (j == blocks - 1) umma_commit(sb + L::kBarQFree);
           }
           __syncwarp();
-          if (j < it.nkb[0] && !(ok = pv(0, j))) break;
+          if (j < nkb[0] && !(ok = pv(0, j, st, par))) break;
+          if (j < blocks) {
+            last = st;
+            lpar = par;
+            if (++st == NST) {
+              st = 0;
+              par ^= 1;
+            }
+          }
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (leader) {
           umma_commit(sb + L::kBarOFull);
-          if (it.nkb[1] > 0) umma_commit(sb + L::kBarOFull + 8);
+          if (nkb[1] > 0) umma_commit(sb + L::kBarOFull + 8);
         }
         __syncwarp();
-        g0 += nkb;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          done[t] += it.nkb[t];
-          items[t] += it.nkb[t] > 0;
+          done[t] += nkb[t];
+          items[t] += nkb[t] > 0;
         }
       }
-      if (lane == 0) umma_commit(sb + L::kBarEnd);
+      if (leader) umma_commit(sb + L::kBarEnd);
       __syncwarp();
       if (!mbar_wait_bounded(sb + L::kBarEnd, 0) && lane == 0)
         record_error(kErrWaitTimeout, blockIdx.x);
