@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (warp == kWarpTma && lane == 0) {
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
@@ -211,6 +211,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   } else if (warp == kWarpMma) {
     // ================= MMA issuer =================
     constexpr uint32_t kId = umma_idesc_f16(BF16, 128, 128, false);
+    const uint32_t tm = warp_uniform(tmem);
+    const uint64_t kdesc = umma_desc_sw128(sb + L::kK, 16, 1024);
+    const uint64_t qdesc = umma_desc_sw128(sb + L::kQ, 16, 1024);
+    const bool leader = elect_lane();
     int nk = 0, nq = 0, ns[2] = {0, 0};
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -219,24 +223,29 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       PwItem it;
       pw_item(a, order, seqs, list, i, it);
       const int ks = nk % L::NK;
+      // the first tile that sees the second key block
+      const int tiles = warp_uniform(it.tiles);
+      int from = tiles;
+      if (it.two)
+        for (from = 0; from < tiles && !pw_sees(it, a.tile_tokens, from, 1);) ++from;
+      from = warp_uniform(from);
       if (!(ok = wait(sb + L::kBarKFull + 8 * ks, (nk / L::NK) & 1))) break;
-      for (int j = 0; j < it.tiles && ok; ++j, ++nq) {
+      for (int j = 0; j < tiles && ok; ++j, ++nq) {
         const int qs = nq % L::NQ;
         if (!(ok = wait(sb + L::kBarQFull + 8 * qs, (nq / L::NQ) & 1))) break;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          if (!pw_sees(it, a.tile_tokens, j, b)) continue;
+          if (b == 1 && j < from) continue;
           const int buf = ns[b] & 1;
           const uint32_t bar = 8 * (2 * b + buf);
           if (ns[b] >= 2 && !(ok = wait(sb + L::kBarSEmpty + bar, ((ns[b] >> 1) & 1) ^ 1))) break;
           tmem_fence_after_sync();
-          if (lane == 0) {
-            const uint32_t kt = sb + L::kK + (ks * 2 + b) * L::kTile, qt = sb + L::kQ + qs * L::kTile;
+          if (leader) {
+            const uint64_t kd = kdesc + (ks * 2 + b) * (L::kTile / 16), qd = qdesc + qs * (L::kTile / 16);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * L::kSlab + (kk & 3) * 32;
-              umma_f16_ss(tmem + 128 * (2 * b + buf), umma_desc_sw128(kt + off, 16, 1024),
-                          umma_desc_sw128(qt + off, 16, 1024), kId, kk > 0 ? 1u : 0u);
+              const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) / 16;
+              umma_f16_ss(tm + 128 * (2 * b + buf), kd + off, qd + off, kId, kk > 0 ? 1u : 0u);
             }
             umma_commit(sb + L::kBarSFull + bar);
           }
@@ -244,15 +253,15 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           ++ns[b];
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (leader) {
           umma_commit(sb + L::kBarQEmpty + 8 * qs);
-          if (j == it.tiles - 1) umma_commit(sb + L::kBarKEmpty + 8 * ks);
+          if (j == tiles - 1) umma_commit(sb + L::kBarKEmpty + 8 * ks);
         }
         __syncwarp();
       }
       ++nk;
     }
-    if (lane == 0) umma_commit(sb + L::kBarEnd);
+    if (leader) umma_commit(sb + L::kBarEnd);
     __syncwarp();
     if (!mbar_wait_bounded(sb + L::kBarEnd, 0) && lane == 0)
       record_error(kErrWaitTimeout, blockIdx.x);
