@@ -153,16 +153,25 @@ def _need(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
-def _on_one_device(stream, *tensors) -> None:
-    """The library launches on the current device: every tensor must be there
-    (and the stream, when it is a torch stream)."""
+# The handle of a device's current stream, without the Stream object around it
+# (3 us a call, as much as a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on_one_device(stream, *tensors) -> int:
+    """The stream to launch on.  The library launches on the current device:
+    every tensor must be there (and the stream, when it is a torch stream)."""
     dev = tensors[0].get_device()       # -1: host memory
     for t in tensors:
         if t.get_device() != dev or dev < 0:
             raise ValueError("tensors must be on one CUDA device")
-    _need(dev == torch.cuda.current_device(), "tensors must be on the current device")
-    if stream is not None and hasattr(stream, "device"):
-        _need(stream.device.index == dev, "stream and tensors must be on one device")
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current device")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    if stream is not None and hasattr(stream, "device") and stream.device.index != dev:
+        raise ValueError("stream and tensors must be on one device")
+    return _stream(stream)
 
 
 # ---------------------------------------------------------------------------
@@ -390,10 +399,30 @@ def pa_prefill(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
 
 
 def _prompt_rows(name, rows, T, D):
-    _need(rows.dim() == 3 and rows.shape[0] == T and rows.shape[2] == D,
-          f"{name} must be [num_tokens, heads, head_dim]")
-    _need(rows.stride()[1:] == (D, 1) or rows.numel() == 0, f"{name} token rows must be dense")
-    return rows.stride(0) if T > 1 else rows.shape[1] * D
+    """The token stride of packed rows [T, heads, D]."""
+    shape, stride = rows.shape, rows.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != D:
+        raise ValueError(f"{name} must be [num_tokens, heads, head_dim]")
+    if (stride[1] != D or stride[2] != 1) and rows.numel():
+        raise ValueError(f"{name} token rows must be dense")
+    return stride[0] if T > 1 else shape[1] * D
+
+
+def _prompt_starts(seq_starts):
+    """The number of sequences."""
+    _need(seq_starts.dtype == torch.int32 and seq_starts.dim() == 1 and
+          seq_starts.shape[0] >= 1 and seq_starts.is_contiguous(),
+          "seq_starts must be [num_seqs + 1] int32")
+    return seq_starts.shape[0] - 1
+
+
+def _weights_columns(weights, S, Hk):
+    """max_tokens of weights [S, Hk, max_tokens] float32."""
+    shape = weights.shape
+    if (len(shape) != 3 or shape[0] != S or shape[1] != Hk or weights.dtype != torch.float32 or
+            not weights.is_contiguous()):
+        raise ValueError("weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
+    return shape[2]
 
 
 def pa_prompt_attention(out: torch.Tensor, lse: torch.Tensor | None, query: torch.Tensor,
@@ -402,25 +431,28 @@ def pa_prompt_attention(out: torch.Tensor, lse: torch.Tensor | None, query: torc
     """Causal attention over packed prompts: query [T, H, D], key/value
     [T, Hk, D] (token rows may be strided), sequence s is rows seq_starts[s] to
     seq_starts[s + 1] - 1; out [T, H, D], lse [T, H] float32 or None."""
-    T, H, D = query.shape
+    shape, dtype = query.shape, query.dtype
+    T, H, D = shape
+    qs = _prompt_rows("query", query, T, D)
+    ks = _prompt_rows("key", key, T, D)
+    vs = _prompt_rows("value", value, T, D)
     Hk = key.shape[1]
-    strides = [_prompt_rows(n, t, T, D) for n, t in
-               (("query", query), ("key", key), ("value", value))]
-    _need(value.shape == key.shape, "key/value shapes differ")
-    _need(query.dtype == key.dtype == value.dtype, "dtype mismatch")
-    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
+    _need(value.shape[1] == Hk, "key/value shapes differ")
+    _need(key.dtype == dtype and value.dtype == dtype, "dtype mismatch")
+    _need(out.shape == shape and out.dtype == dtype and out.is_contiguous(),
           "out must be [num_tokens, num_heads, head_dim] contiguous")
-    _need(lse is None or (lse.dtype == torch.float32 and lse.shape == (T, H) and
-                          lse.is_contiguous()), "lse must be [num_tokens, num_heads] float32")
-    _need(seq_starts.dtype == torch.int32 and seq_starts.dim() == 1 and
-          seq_starts.shape[0] >= 1 and seq_starts.is_contiguous(),
-          "seq_starts must be [num_seqs + 1] int32")
+    S = _prompt_starts(seq_starts)
     dt = _dtype_code(query)
-    _on_one_device(stream, query, key, value, out, seq_starts, *([] if lse is None else [lse]))
-    st = load().pa_prompt_attention(out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                    query.data_ptr(), key.data_ptr(), value.data_ptr(), *strides,
-                                    seq_starts.data_ptr(), float(scale), seq_starts.shape[0] - 1,
-                                    T, H, Hk, D, dt, _stream(stream))
+    if lse is None:
+        at, s = None, _stream_on_one_device(stream, query, key, value, out, seq_starts)
+    else:
+        _need(lse.dtype == torch.float32 and lse.shape == shape[:2] and lse.is_contiguous(),
+              "lse must be [num_tokens, num_heads] float32")
+        at = lse.data_ptr()
+        s = _stream_on_one_device(stream, query, key, value, out, seq_starts, lse)
+    st = load().pa_prompt_attention(out.data_ptr(), at, query.data_ptr(), key.data_ptr(),
+                                    value.data_ptr(), qs, ks, vs, seq_starts.data_ptr(), float(scale), S,
+                                    T, H, Hk, D, dt, s)
     _check(st, "pa_prompt_attention")
 
 
@@ -430,25 +462,21 @@ def pa_prompt_weights(weights: torch.Tensor, query: torch.Tensor, key: torch.Ten
     """The attention weight each token of a packed prompt receives from the last
     `window` tokens of its sequence, into weights [S, Hk, max_tokens] float32;
     query, key, seq_starts and scale as pa_prompt_attention, lse as it wrote it."""
-    T, H, D = query.shape
+    shape = query.shape
+    T, H, D = shape
+    qs = _prompt_rows("query", query, T, D)
+    ks = _prompt_rows("key", key, T, D)
     Hk = key.shape[1]
-    strides = [_prompt_rows(n, t, T, D) for n, t in (("query", query), ("key", key))]
     _need(query.dtype == key.dtype, "dtype mismatch")
-    _need(lse.dtype == torch.float32 and lse.shape == (T, H) and lse.is_contiguous(),
+    _need(lse.dtype == torch.float32 and lse.shape == shape[:2] and lse.is_contiguous(),
           "lse must be [num_tokens, num_heads] float32")
-    _need(seq_starts.dtype == torch.int32 and seq_starts.dim() == 1 and
-          seq_starts.shape[0] >= 1 and seq_starts.is_contiguous(),
-          "seq_starts must be [num_seqs + 1] int32")
-    S = seq_starts.shape[0] - 1
-    _need(weights.dtype == torch.float32 and weights.dim() == 3 and
-          weights.shape[:2] == (S, Hk) and weights.is_contiguous(),
-          "weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
+    S = _prompt_starts(seq_starts)
+    W = _weights_columns(weights, S, Hk)
     dt = _dtype_code(query)
-    _on_one_device(stream, query, key, lse, weights, seq_starts)
+    s = _stream_on_one_device(stream, query, key, lse, weights, seq_starts)
     st = load().pa_prompt_weights(weights.data_ptr(), query.data_ptr(), key.data_ptr(),
-                                  lse.data_ptr(), *strides, seq_starts.data_ptr(), float(scale),
-                                  S, T, H, Hk, D, weights.shape[2], int(window), dt,
-                                  _stream(stream))
+                                  lse.data_ptr(), qs, ks, seq_starts.data_ptr(), float(scale), S, T, H,
+                                  Hk, D, W, int(window), dt, s)
     _check(st, "pa_prompt_weights")
 
 
@@ -463,36 +491,38 @@ def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, workspace, query
                                                     block_tables, context_lens)
     _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
           "out must match query")
-    _need(weights.dtype == torch.float32 and weights.dim() == 3 and
-          weights.shape[:2] == (S, Hk) and weights.is_contiguous(),
-          "weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
+    W = _weights_columns(weights, S, Hk)
     _need(context_lens.is_contiguous(), "context_lens must be contiguous")
     buf = workspace.buffer
-    _on_one_device(stream, query, out, weights, buf, key_cache, value_cache, block_tables,
-                   context_lens)
+    s = _stream_on_one_device(stream, query, out, weights, buf, key_cache, value_cache,
+                              block_tables, context_lens)
     st = load().pa_decode_weights(out.data_ptr(), weights.data_ptr(), buf.data_ptr(), buf.numel(),
                                   query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-                                  block_tables.data_ptr(), context_lens.data_ptr(), float(scale),
-                                  S, H, Hk, D, NB, bs, MB, weights.shape[2], int(new_tokens), dt,
-                                  _stream(stream))
+                                  block_tables.data_ptr(), context_lens.data_ptr(), float(scale), S, H,
+                                  Hk, D, NB, bs, MB, W, int(new_tokens), dt, s)
     _check(st, "pa_decode_weights")
 
 
 def _evict_common(weights, positions, source, new_lens, context_lens, recorded_lens, seq_lens):
-    _need(weights.dtype == torch.float32 and weights.dim() == 3 and weights.is_contiguous(),
-          "weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
-    S, Hk, W = weights.shape
-    _need(positions.dtype == torch.int32 and positions.shape == weights.shape and
-          positions.is_contiguous(), "positions must be int32, shaped like weights")
-    _need(source.dtype == torch.int32 and source.dim() == 3 and source.shape[:2] == (S, Hk) and
-          source.is_contiguous(), "source must be [num_seqs, num_kv_heads, budget] int32")
-    for name, t in (("new_lens", new_lens), ("context_lens", context_lens),
-                    ("recorded_lens", recorded_lens), ("seq_lens", seq_lens)):
-        _need(t.dtype == torch.int32 and t.shape == (S,) and t.is_contiguous(),
-              f"{name} must be [num_seqs] int32")
-    _need(new_lens.data_ptr() not in (context_lens.data_ptr(), recorded_lens.data_ptr()) or S == 0,
-          "new_lens must not share storage with context_lens or recorded_lens")
-    return S, Hk, W, source.shape[2]
+    shape, i32 = weights.shape, torch.int32
+    if len(shape) != 3 or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError("weights must be [num_seqs, num_kv_heads, max_tokens] float32 contiguous")
+    if positions.dtype != i32 or positions.shape != shape or not positions.is_contiguous():
+        raise ValueError("positions must be int32, shaped like weights")
+    S, Hk, W = shape
+    budget = source.shape
+    if (source.dtype != i32 or len(budget) != 3 or budget[0] != S or budget[1] != Hk or
+            not source.is_contiguous()):
+        raise ValueError("source must be [num_seqs, num_kv_heads, budget] int32")
+    for t in (new_lens, context_lens, recorded_lens, seq_lens):
+        if t.dtype != i32 or t.shape != (S,) or not t.is_contiguous():
+            raise ValueError("new_lens, context_lens, recorded_lens and seq_lens must be "
+                             "[num_seqs] int32")
+    at = new_lens.data_ptr()
+    if S and (at == context_lens.data_ptr() or at == recorded_lens.data_ptr() or
+              at == seq_lens.data_ptr()):
+        raise ValueError("new_lens must not share storage with the lengths it is found from")
+    return S, Hk, W, budget[2]
 
 
 def pa_evict_select(source: torch.Tensor, new_lens: torch.Tensor, weights: torch.Tensor,
@@ -504,12 +534,12 @@ def pa_evict_select(source: torch.Tensor, new_lens: torch.Tensor, weights: torch
     from; new_lens [S] int32 the packed lengths."""
     S, Hk, W, B = _evict_common(weights, positions, source, new_lens, context_lens,
                                 recorded_lens, seq_lens)
-    _on_one_device(stream, weights, positions, source, new_lens, context_lens, recorded_lens,
-                   seq_lens)
+    s = _stream_on_one_device(stream, weights, positions, source, new_lens, context_lens,
+                              recorded_lens, seq_lens)
     st = load().pa_evict_select(source.data_ptr(), new_lens.data_ptr(), weights.data_ptr(),
                                 positions.data_ptr(), context_lens.data_ptr(),
-                                recorded_lens.data_ptr(), seq_lens.data_ptr(), S, Hk, W, B,
-                                int(sink), int(recent), _stream(stream))
+                                recorded_lens.data_ptr(), seq_lens.data_ptr(), S, Hk, W, B, int(sink),
+                                int(recent), s)
     _check(st, "pa_evict_select")
 
 
@@ -521,22 +551,23 @@ def pa_evict_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, weights
     first new_lens[s] slots; caches [NB, bs, Hk, D] contiguous, 16-bit or uint8."""
     S, Hk, W, B = _evict_common(weights, positions, source, new_lens, context_lens,
                                 recorded_lens, seq_lens)
-    NB, bs, Hk2, D = key_cache.shape
+    shape = key_cache.shape
+    NB, bs, Hk2, D = shape
     _need(Hk2 == Hk, "caches and weights differ in num_kv_heads")
-    _need(value_cache.shape == key_cache.shape and key_cache.dtype == value_cache.dtype,
+    _need(value_cache.shape == shape and key_cache.dtype == value_cache.dtype,
           "key/value caches differ")
     _need(key_cache.is_contiguous() and value_cache.is_contiguous(), "caches must be contiguous")
     _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and
           block_tables.shape[0] == S and block_tables.is_contiguous(),
           "block_tables must be [num_seqs, max_blocks] int32 contiguous")
-    _on_one_device(stream, key_cache, value_cache, weights, positions, source, new_lens,
-                   block_tables, context_lens, recorded_lens, seq_lens)
+    s = _stream_on_one_device(stream, key_cache, value_cache, weights, positions, source, new_lens,
+                              block_tables, context_lens, recorded_lens, seq_lens)
     st = load().pa_evict_compact(key_cache.data_ptr(), value_cache.data_ptr(),
                                  weights.data_ptr(), positions.data_ptr(), source.data_ptr(),
                                  new_lens.data_ptr(), block_tables.data_ptr(),
                                  context_lens.data_ptr(), recorded_lens.data_ptr(),
                                  seq_lens.data_ptr(), S, Hk, D, NB, bs, block_tables.shape[1], W,
-                                 B, key_cache.element_size(), _stream(stream))
+                                 B, key_cache.element_size(), s)
     _check(st, "pa_evict_compact")
 
 
