@@ -115,6 +115,30 @@ __device__ __forceinline__ bool elect_lane() {
 // the compiler takes for a lane's own is moved there for every MMA.
 __device__ __forceinline__ int warp_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// 2^x of two values as p * s on the FMA pipe, for part of the elements where the
+// special-function unit (16 results a cycle and SM) would bound: with n the
+// nearest integer of x, s = 2^n and p a polynomial of degree 5 for 2^(x - n),
+// the minimax fit of the relative error on [-1/2, 1/2] (7.5e-8, 2.1e-7 in fp32).
+// x is taken as at least -126 (2^-126 for less); a NaN stays one, +inf gives NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void exp2_fma(float2 x, float2& p, float2& s) {
+  auto both = [](float v) { return make_float2(v, v); };
+  x = make_float2(max_nan(x.x, -126.f), max_nan(x.y, -126.f));
+  const float2 t = ffma2(x, both(1.f), both(12582912.f));          // 1.5 * 2^23 + n
+  const float2 f = ffma2(ffma2(t, both(1.f), both(-12582912.f)), both(-1.f), x);
+  p = ffma2(f, both(0.0013276472454890609f), both(0.009675540961325169f));
+  p = ffma2(p, f, both(0.05550713092088699f));
+  p = ffma2(p, f, both(0.24022120237350464f));
+  p = ffma2(p, f, both(0.6931469440460205f));
+  p = ffma2(p, f, both(1.0000001192092896f));
+  s = make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
+                  __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u));
+}
+
 // Store 32 32-bit columns of this thread's lane (complete after tmem_wait_st).
 __device__ __forceinline__ void tmem_st32u_async(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(

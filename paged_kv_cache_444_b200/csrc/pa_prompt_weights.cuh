@@ -11,20 +11,25 @@
 // over its columns in registers; nothing is shuffled, no sum leaves the thread
 // before it is written, and the order of the additions is fixed.
 //
-// Work item: (sequence, KV head, two blocks of 128 keys).  The item's K stays in
+// Work item: (sequence, KV head, four blocks of 128 keys).  The item's K stays in
 // shared memory while the query tiles stream through a ring, each loaded once
-// for both key blocks.  One consumer warpgroup a key block, two S^T buffers
-// each, so that the next tile's product runs during this one's 2^x.  Warps: 0-3
-// and 4-7 the key blocks, 8 issues the MMAs, 9 the loads, 10 brings each tile's
-// lse into shared memory (negated, in log2 units).
+// for the four key blocks.  One consumer warpgroup a key block: it frees its S^T
+// as soon as that is in registers, so that the next tile's product runs during
+// the 2^x, and the four together keep four warps on each scheduler, which is what
+// bounds it (2^x takes 8 cycles of a scheduler's special-function unit for 32
+// elements; 3 of 8 run on the FMA pipe instead).  Warps: 0-15 the key blocks, 16
+// issues the MMAs, 17 the loads, 18 brings each tile's lse into shared memory
+// (negated, in log2 units).
 #pragma once
 
 #include "pa_prompt.cuh"
 
 namespace pa {
 
-constexpr int kPwThreads = 11 * 32;
-constexpr int kPwSpan = 256;       // keys of an item
+constexpr int kPwBlocks = 4;                    // key blocks of an item
+constexpr int kPwSpan = 128 * kPwBlocks;        // keys of an item
+constexpr int kPwThreads = (4 * kPwBlocks + 3) * 32;
+constexpr int kPwWarpMma = 4 * kPwBlocks, kPwWarpTma = kPwWarpMma + 1, kPwWarpLse = kPwWarpMma + 2;
 
 struct PromptWeightsArgs {
   float* weights;              // [S, Hk, max_tokens]
@@ -46,21 +51,20 @@ struct PwSmem {
   static constexpr int kSlabs = D / 64;
   static constexpr int kSlab = 128 * 128;
   static constexpr int kTile = kSlabs * kSlab;        // one key block, or one query tile
-  static constexpr int NK = 2;                        // items' K in flight
   static constexpr int NQ = D == 64 ? 4 : 2;          // query tiles in flight
   static constexpr int NL = 4;                        // tiles' lse in flight
   static constexpr int kK = 0;
-  static constexpr int kQ = kK + NK * 2 * kTile;
+  static constexpr int kQ = kK + kPwBlocks * kTile;
   static constexpr int kLse = kQ + NQ * kTile;        // NL x 128 floats
-  static constexpr int kBarKFull = kLse + NL * 512;
-  static constexpr int kBarKEmpty = kBarKFull + 8 * NK;
-  static constexpr int kBarQFull = kBarKEmpty + 8 * NK;
+  static constexpr int kBarKFull = kLse + NL * 512;   // per key block
+  static constexpr int kBarKEmpty = kBarKFull + 8 * kPwBlocks;
+  static constexpr int kBarSFull = kBarKEmpty + 8 * kPwBlocks;
+  static constexpr int kBarSEmpty = kBarSFull + 8 * kPwBlocks;
+  static constexpr int kBarQFull = kBarSEmpty + 8 * kPwBlocks;
   static constexpr int kBarQEmpty = kBarQFull + 8 * NQ;
   static constexpr int kBarLFull = kBarQEmpty + 8 * NQ;
   static constexpr int kBarLEmpty = kBarLFull + 8 * NL;
-  static constexpr int kBarSFull = kBarLEmpty + 8 * NL;   // [block][buffer]
-  static constexpr int kBarSEmpty = kBarSFull + 8 * 4;
-  static constexpr int kBarEnd = kBarSEmpty + 8 * 4;
+  static constexpr int kBarEnd = kBarLEmpty + 8 * NL;
   static constexpr int kTmemSlot = kBarEnd + 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kSched = kAbort + 4;
@@ -75,7 +79,7 @@ struct PwItem {
   int s, kvh, q0, len;   // sequence, KV head, its first row and its length
   int k0;                // first key
   int t0, tiles;         // first query token and the number of query tiles
-  bool two;              // a second key block
+  int blocks;            // key blocks
 };
 
 // The pairs of a sequence are ranked as the attention's are (more keys, more
@@ -91,12 +95,33 @@ __device__ __forceinline__ void pw_item(const PromptWeightsArgs& a, const Prompt
   it.k0 = ((it.len + kPwSpan - 1) / kPwSpan - 1 - unit.y) * kPwSpan;
   it.t0 = max(it.k0, it.len - a.window);
   it.tiles = (it.len - it.t0 + a.tile_tokens - 1) / a.tile_tokens;
-  it.two = it.k0 + 128 < it.len;
+  it.blocks = min(kPwBlocks, (it.len - it.k0 + 127) / 128);
 }
 
-// Whether tile i's tokens see any key of block b.
-__device__ __forceinline__ bool pw_sees(const PwItem& it, int tile_tokens, int i, int b) {
-  return b == 0 || (it.two && min(it.t0 + (i + 1) * tile_tokens, it.len) > it.k0 + 128);
+// The first query tile that sees a key of block b.
+__device__ __forceinline__ int pw_first(const PwItem& it, int tile_tokens, int b) {
+  return max(0, it.k0 + 128 * b - it.t0) / tile_tokens;
+}
+
+// sum += 2^(s scale + neg) over 32 columns, three pairs of eight on the FMA
+// pipe and the others on the special-function unit.
+__device__ __forceinline__ void add_columns(const float (&s)[32], const float4* neg4, float2 scale,
+                                            float2 (&sum)[2]) {
+  const float2 one = make_float2(1.f, 1.f);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 neg = neg4[q];
+    const float2 x = ffma2(make_float2(s[4 * q], s[4 * q + 1]), scale, make_float2(neg.x, neg.y));
+    const float2 y = ffma2(make_float2(s[4 * q + 2], s[4 * q + 3]), scale, make_float2(neg.z, neg.w));
+    if (q % 4 != 0) {
+      float2 p, e;
+      exp2_fma(x, p, e);
+      sum[0] = ffma2(p, e, sum[0]);
+    } else {
+      sum[0] = ffma2(make_float2(ex2(x.x), ex2(x.y)), one, sum[0]);
+    }
+    sum[1] = ffma2(make_float2(ex2(y.x), ex2(y.y)), one, sum[1]);
+  }
 }
 
 template <int D, bool BF16>
@@ -109,7 +134,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_addr(smem);
   const int warp = warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (warp == kWarpTma && lane == 0) {
+  if (warp == kPwWarpTma && lane == 0) {
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
   }
@@ -128,9 +153,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::NK; ++i) {
+    for (int i = 0; i < kPwBlocks; ++i) {
       mbar_init(sb + L::kBarKFull + 8 * i, 1);
       mbar_init(sb + L::kBarKEmpty + 8 * i, 1);
+      mbar_init(sb + L::kBarSFull + 8 * i, 1);
+      mbar_init(sb + L::kBarSEmpty + 8 * i, 128);
     }
     for (int i = 0; i < L::NQ; ++i) {
       mbar_init(sb + L::kBarQFull + 8 * i, 1);
@@ -138,20 +165,16 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     }
     for (int i = 0; i < L::NL; ++i) {
       mbar_init(sb + L::kBarLFull + 8 * i, 32);
-      mbar_init(sb + L::kBarLEmpty + 8 * i, 256);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(sb + L::kBarSFull + 8 * i, 1);
-      mbar_init(sb + L::kBarSEmpty + 8 * i, 128);
+      mbar_init(sb + L::kBarLEmpty + 8 * i, 128 * kPwBlocks);
     }
     mbar_init(sb + L::kBarEnd, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpMma) tmem_alloc(sb + L::kTmemSlot, kTmemCols);
-  if (warp < 8 && q_rows < 128) {   // rows no query box covers: finite (their lse is +inf)
+  if (warp == kPwWarpMma) tmem_alloc(sb + L::kTmemSlot, kTmemCols);
+  if (warp < kPwWarpMma && q_rows < 128) {   // rows no query box covers: finite (their lse is +inf)
     const int chunks = (128 - q_rows) * 8;
-    for (int i = threadIdx.x; i < chunks * L::kSlabs * L::NQ; i += 256) {
+    for (int i = threadIdx.x; i < chunks * L::kSlabs * L::NQ; i += 128 * kPwBlocks) {
       const int b = i / chunks, c = i % chunks;
       sts128(sb + L::kQ + b * L::kSlab + q_rows * 128 + c * 16, 0u, 0u, 0u, 0u);
     }
@@ -165,30 +188,30 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag)) != 0;
   };
 
-  if (warp == kWarpTma) {
+  if (warp == kPwWarpTma) {
     // ================= loads =================
-    int nk = 0, nq = 0;
+    int nk[kPwBlocks] = {}, nq = 0;      // items so far with each key block, query tiles
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
       if (i < 0) break;
       PwItem it;
       pw_item(a, order, seqs, list, i, it);
-      const int ks = nk % L::NK;
-      if (nk >= L::NK && !(ok = wait(sb + L::kBarKEmpty + 8 * ks, ((nk / L::NK) & 1) ^ 1))) break;
-      if (lane == 0) {
-        const int blocks = it.two ? 2 : 1;
-        mbar_arrive_expect_tx(sb + L::kBarKFull + 8 * ks, blocks * L::kTile);
-        for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+      for (int b = 0; b < kPwBlocks; ++b) {
+        if (b >= it.blocks || !ok) continue;
+        if (nk[b] > 0 && !(ok = wait(sb + L::kBarKEmpty + 8 * b, (nk[b] - 1) & 1))) continue;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(sb + L::kBarKFull + 8 * b, L::kTile);
 #pragma unroll
           for (int c = 0; c < L::kSlabs; ++c)
-            tma_load_4d(sb + L::kK + (ks * 2 + b) * L::kTile + c * L::kSlab, &kmap,
-                        sb + L::kBarKFull + 8 * ks, 0, c, it.kvh, it.q0 + it.k0 + 128 * b);
+            tma_load_4d(sb + L::kK + b * L::kTile + c * L::kSlab, &kmap,
+                        sb + L::kBarKFull + 8 * b, 0, c, it.kvh, it.q0 + it.k0 + 128 * b);
         }
+        __syncwarp();
+        ++nk[b];
       }
-      __syncwarp();
-      ++nk;
-      for (int j = 0; j < it.tiles; ++j) {
+      for (int j = 0; j < it.tiles && ok; ++j) {
         const int qs = nq % L::NQ;
         if (nq >= L::NQ && !(ok = wait(sb + L::kBarQEmpty + 8 * qs, ((nq / L::NQ) & 1) ^ 1))) break;
         if (lane == 0) {
@@ -204,68 +227,63 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
     }
     // every load issued lands before the CTA can exit
-    for (int g = max(0, nk - L::NK); g < nk; ++g)
-      mbar_wait_bounded(sb + L::kBarKFull + 8 * (g % L::NK), (g / L::NK) & 1);
+#pragma unroll
+    for (int b = 0; b < kPwBlocks; ++b)
+      if (nk[b] > 0) mbar_wait_bounded(sb + L::kBarKFull + 8 * b, (nk[b] - 1) & 1);
     for (int g = max(0, nq - L::NQ); g < nq; ++g)
       mbar_wait_bounded(sb + L::kBarQFull + 8 * (g % L::NQ), (g / L::NQ) & 1);
-  } else if (warp == kWarpMma) {
+  } else if (warp == kPwWarpMma) {
     // ================= MMA issuer =================
     constexpr uint32_t kId = umma_idesc_f16(BF16, 128, 128, false);
     const uint32_t tm = warp_uniform(tmem);
     const uint64_t kdesc = umma_desc_sw128(sb + L::kK, 16, 1024);
     const uint64_t qdesc = umma_desc_sw128(sb + L::kQ, 16, 1024);
     const bool leader = elect_lane();
-    int nk = 0, nq = 0, ns[2] = {0, 0};
+    int nk[kPwBlocks] = {}, ns[kPwBlocks] = {}, nq = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
       if (i < 0) break;
       PwItem it;
       pw_item(a, order, seqs, list, i, it);
-      const int ks = nk % L::NK;
-      // the first tile that sees the second key block
-      const int tiles = warp_uniform(it.tiles);
-      int from = tiles;
-      if (it.two)
-        for (from = 0; from < tiles && !pw_sees(it, a.tile_tokens, from, 1);) ++from;
-      from = warp_uniform(from);
-      if (!(ok = wait(sb + L::kBarKFull + 8 * ks, (nk / L::NK) & 1))) break;
+      const int tiles = warp_uniform(it.tiles), blocks = warp_uniform(it.blocks);
+      int first[kPwBlocks];
+#pragma unroll
+      for (int b = 0; b < kPwBlocks; ++b) first[b] = warp_uniform(pw_first(it, a.tile_tokens, b));
       for (int j = 0; j < tiles && ok; ++j, ++nq) {
         const int qs = nq % L::NQ;
         if (!(ok = wait(sb + L::kBarQFull + 8 * qs, (nq / L::NQ) & 1))) break;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (b == 1 && j < from) continue;
-          const int buf = ns[b] & 1;
-          const uint32_t bar = 8 * (2 * b + buf);
-          if (ns[b] >= 2 && !(ok = wait(sb + L::kBarSEmpty + bar, ((ns[b] >> 1) & 1) ^ 1))) break;
+        for (int b = 0; b < kPwBlocks; ++b) {
+          if (b >= blocks || j < first[b] || !ok) continue;
+          if (j == first[b] && !(ok = wait(sb + L::kBarKFull + 8 * b, nk[b] & 1))) continue;
+          if (ns[b] > 0 && !(ok = wait(sb + L::kBarSEmpty + 8 * b, (ns[b] - 1) & 1))) continue;
           tmem_fence_after_sync();
           if (leader) {
-            const uint64_t kd = kdesc + (ks * 2 + b) * (L::kTile / 16), qd = qdesc + qs * (L::kTile / 16);
+            const uint64_t kd = kdesc + b * (L::kTile / 16), qd = qdesc + qs * (L::kTile / 16);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) / 16;
-              umma_f16_ss(tm + 128 * (2 * b + buf), kd + off, qd + off, kId, kk > 0 ? 1u : 0u);
+              umma_f16_ss(tm + 128 * b, kd + off, qd + off, kId, kk > 0 ? 1u : 0u);
             }
-            umma_commit(sb + L::kBarSFull + bar);
+            umma_commit(sb + L::kBarSFull + 8 * b);
+            if (j == tiles - 1) umma_commit(sb + L::kBarKEmpty + 8 * b);
           }
           __syncwarp();
           ++ns[b];
         }
         if (!ok) break;
-        if (leader) {
-          umma_commit(sb + L::kBarQEmpty + 8 * qs);
-          if (j == tiles - 1) umma_commit(sb + L::kBarKEmpty + 8 * ks);
-        }
+        if (leader) umma_commit(sb + L::kBarQEmpty + 8 * qs);
         __syncwarp();
       }
-      ++nk;
+#pragma unroll
+      for (int b = 0; b < kPwBlocks; ++b) nk[b] += b < blocks;
     }
     if (leader) umma_commit(sb + L::kBarEnd);
     __syncwarp();
     if (!mbar_wait_bounded(sb + L::kBarEnd, 0) && lane == 0)
       record_error(kErrWaitTimeout, blockIdx.x);
-  } else if (warp == 10) {
+  } else if (warp == kPwWarpLse) {
     // ================= the tiles' lse =================
     int n = 0;
     bool ok = true;
@@ -294,11 +312,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
     }
   } else {
-    // ================= key block b = warp / 4, key = tensor-memory lane =================
+    // ================= key block b, key = tensor-memory lane =================
     const int b = warp >> 2, key = threadIdx.x & 127;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 * b;
     const float2 scale = make_float2(a.scale_log2, a.scale_log2);
-    const float2 one = make_float2(1.f, 1.f);
     int n = 0, ns = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -307,52 +324,52 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       PwItem it;
       pw_item(a, order, seqs, list, i, it);
       const int kb = it.k0 + 128 * b, kj = kb + key;
+      const int first = b < it.blocks ? pw_first(it, a.tile_tokens, b) : it.tiles;
       float acc = 0.f;
       for (int j = 0; j < it.tiles; ++j, ++n) {
         const int sl = n % L::NL;
         if (!(ok = wait(sb + L::kBarLFull + 8 * sl, (n / L::NL) & 1))) break;
-        if (pw_sees(it, a.tile_tokens, j, b)) {
-          const int buf = ns & 1;
-          const uint32_t bar = 8 * (2 * b + buf);
-          if (!(ok = wait(sb + L::kBarSFull + bar, (ns >> 1) & 1))) break;
+        if (j >= first) {
+          if (!(ok = wait(sb + L::kBarSFull + 8 * b, ns & 1))) break;
           tmem_fence_after_sync();
           const int tok0 = it.t0 + j * a.tile_tokens;
           const int rows = min(a.tile_tokens, it.len - tok0) * G;
-          // columns of tokens before this key, or past the tile's rows, do not count
-          const int c0 = max(0, kj - tok0) * G;
-          const bool masked = rows < 128 || tok0 < kb + 127;
           const float4* lse4 = reinterpret_cast<const float4*>(lse_sh + sl * 128);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          if (rows == q_rows && tok0 >= kb + 127) {
+            // every column counts (those past q_rows have an lse of +inf)
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              float u[32];
+              tmem_ld32(s_addr + 32 * h, u);
+              if (h == 3) {
+                tmem_fence_before_sync();
+                mbar_arrive(sb + L::kBarSEmpty + 8 * b);   // S is in registers
+              }
+              add_columns(u, lse4 + 8 * h, scale, sum);
+            }
+          } else {
+            // columns of tokens before this key, or past the tile's rows, do not count
+            const int c0 = max(0, kj - tok0) * G;
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              float s[32];
+              tmem_ld32(s_addr + 32 * h, s);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float s[32];
-            tmem_ld32(t_lane + 128 * (2 * b + buf) + 32 * h, s);
-            if (masked) {
+              for (int q = 0; q < 8; ++q) {
+                const float4 neg = lse4[8 * h + q];
+                const float n4[4] = {neg.x, neg.y, neg.z, neg.w};
 #pragma unroll
-              for (int q = 0; q < 32; ++q) {
-                const int c = 32 * h + q;
-                s[q] = c >= c0 && c < rows ? s[q] : 0.f;
+                for (int e = 0; e < 4; ++e) {
+                  const int c = 32 * h + 4 * q + e;
+                  const float v = ex2(s[4 * q + e] * a.scale_log2 + n4[e]);
+                  sum[e & 1].x += c >= c0 && c < rows ? v : 0.f;
+                }
               }
             }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 neg = lse4[8 * h + q];
-              float2 x = ffma2(make_float2(s[4 * q], s[4 * q + 1]), scale, make_float2(neg.x, neg.y));
-              float2 y = ffma2(make_float2(s[4 * q + 2], s[4 * q + 3]), scale, make_float2(neg.z, neg.w));
-              float2 e = make_float2(ex2(x.x), ex2(x.y)), f = make_float2(ex2(y.x), ex2(y.y));
-              if (masked) {
-                const int c = 32 * h + 4 * q;
-                e.x = c >= c0 ? e.x : 0.f;
-                e.y = c + 1 >= c0 ? e.y : 0.f;
-                f.x = c + 2 >= c0 ? f.x : 0.f;
-                f.y = c + 3 >= c0 ? f.y : 0.f;
-              }
-              sum[0] = ffma2(e, one, sum[0]);
-              sum[1] = ffma2(f, one, sum[1]);
-            }
+            tmem_fence_before_sync();
+            mbar_arrive(sb + L::kBarSEmpty + 8 * b);
           }
-          tmem_fence_before_sync();
-          mbar_arrive(sb + L::kBarSEmpty + bar);
           acc += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           ++ns;
         }
@@ -361,7 +378,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       if (!ok) break;
       if (it.len > a.max_tokens) {
         if (key == 0 && b == 0 && it.k0 == 0 && it.kvh == 0) record_error(kErrContextLen, it.s);
-      } else if (kj < it.len) {
+      } else if (kj < it.len && b < it.blocks) {
         a.weights[(static_cast<size_t>(it.s) * a.num_kv_heads + it.kvh) * a.max_tokens + kj] = acc;
       }
     }
@@ -369,7 +386,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   tmem_fence_before_sync();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == kPwWarpMma) {
     tmem_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
