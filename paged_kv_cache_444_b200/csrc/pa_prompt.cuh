@@ -30,6 +30,8 @@
 // its epilogues add such values to the rows that do see them.
 #pragma once
 
+#include <limits.h>
+
 #include "pa_prefill.cuh"
 
 namespace pa {
@@ -84,8 +86,8 @@ struct PromptSmem {
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kMark = kAbort + 4;               // a V value that is not finite was met
   static constexpr int kSched = kMark + 4;               // unit count and per-warp sums
-  static constexpr int kSeqs = (kSched + 128 + 15) & ~15;      // int2 per ranked sequence
-  static constexpr int kList = kSeqs + 8 * kPromptRankSeqs;    // unit of each rank
+  static constexpr int kSeqs = (kSched + 128 + 15) & ~15;      // int4 per ranked sequence
+  static constexpr int kList = kSeqs + 16 * kPromptRankSeqs;   // unit of each rank
   static constexpr int kBytes = kList + 4 * kPromptRankUnits;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -180,11 +182,11 @@ struct PromptOrder {
 // with bad bounds has no units and is reported by one CTA.
 template <class Args>
 __device__ __forceinline__ PromptOrder prompt_order(const Args& a, int span, int* sched,
-                                                    int2* seqs, int* list, int warp, int lane) {
+                                                    int4* seqs, int* list, int warp, int lane) {
   const int t = threadIdx.x, n = static_cast<int>(blockDim.x);
   const bool table = a.num_seqs <= kPromptRankSeqs;
   const int chunk = (a.num_seqs + n - 1) / n;     // 1 for a table
-  int mine = 0, len0 = 0;
+  int mine = 0, len0 = 0;                        // a table entry: length, first unit, first row
   for (int s = t * chunk; s < min(a.num_seqs, (t + 1) * chunk); ++s) {
     const int len = prompt_len(a.seq_starts, s, a.num_tokens);
     if (len < 0) {
@@ -205,7 +207,7 @@ __device__ __forceinline__ PromptOrder prompt_order(const Args& a, int span, int
   for (int w = 0; w < warp; ++w) first += sched[4 + w];
   if (t == n - 1) sched[0] = first;
   first -= mine;
-  if (table && t < a.num_seqs) seqs[t] = make_int2(len0, first);
+  if (table && t < a.num_seqs) seqs[t] = make_int4(len0, first, a.seq_starts[t], 0);
   if (!table) list[t] = first;
   __syncthreads();
   PromptOrder o;
@@ -238,11 +240,18 @@ __device__ __forceinline__ PromptOrder prompt_order(const Args& a, int span, int
   return o;
 }
 
-// Unit u as (sequence, pair).
+struct PromptUnit {
+  int s, pair, q0, len;    // sequence, its pair, first row and length
+};
+
 template <class Args>
-__device__ __forceinline__ int2 prompt_unit(const Args& a, const PromptOrder& o, const int2* seqs,
-                                            const int* list, int u, int span) {
-  if (o.ranked) return make_int2(list[u] & 0xffff, list[u] >> 16);
+__device__ __forceinline__ PromptUnit prompt_unit(const Args& a, const PromptOrder& o,
+                                                  const int4* seqs, const int* list, int u,
+                                                  int span) {
+  if (o.ranked) {
+    const int e = list[u], s = e & 0xffff;
+    return {s, e >> 16, seqs[s].z, seqs[s].x};
+  }
   if (a.num_seqs <= kPromptRankSeqs) {
     int lo = 0, hi = a.num_seqs;
     while (hi - lo > 1) {
@@ -250,7 +259,7 @@ __device__ __forceinline__ int2 prompt_unit(const Args& a, const PromptOrder& o,
       if (seqs[mid].y <= u) lo = mid;
       else hi = mid;
     }
-    return make_int2(lo, u - seqs[lo].y);
+    return {lo, u - seqs[lo].y, seqs[lo].z, seqs[lo].x};
   }
   const int n = static_cast<int>(blockDim.x), chunk = (a.num_seqs + n - 1) / n;
   int lo = 0, hi = n;                  // the last chunk whose first unit is <= u
@@ -265,7 +274,8 @@ __device__ __forceinline__ int2 prompt_unit(const Args& a, const PromptOrder& o,
     if (u < first + units || s + 1 >= a.num_seqs) break;
     first += units;
   }
-  return make_int2(s, u - first);
+  const int q0 = a.seq_starts[s];
+  return {s, u - first, q0, a.seq_starts[s + 1] - q0};
 }
 
 struct PromptItem {
@@ -273,16 +283,15 @@ struct PromptItem {
 };
 
 __device__ __forceinline__ void prompt_item(const PromptArgs& a, const PromptOrder& o,
-                                            const int2* seqs, const int* list, int i, int span,
+                                            const int4* seqs, const int* list, int i, int span,
                                             PromptItem& it) {
   const int u = i / a.num_kv_heads;
   it.kvh = i - u * a.num_kv_heads;
-  const int2 unit = prompt_unit(a, o, seqs, list, u, span);
-  const int p = unit.y;
-  it.s = unit.x;
-  it.q0 = a.seq_starts[it.s];
-  it.len = a.seq_starts[it.s + 1] - it.q0;
-  it.tile_a = p * span;
+  const PromptUnit unit = prompt_unit(a, o, seqs, list, u, span);
+  it.s = unit.s;
+  it.q0 = unit.q0;
+  it.len = unit.len;
+  it.tile_a = unit.pair * span;
   const int half = span / 2;
   it.lim[0] = min(it.tile_a + half, it.len);
   it.lim[1] = it.tile_a + half < it.len ? min(it.tile_a + span, it.len) : 0;
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   pdl_wait();
 
   const int G = a.group, span = 2 * a.tile_tokens;
-  int2* seqs = reinterpret_cast<int2*>(smem + L::kSeqs);
+  int4* seqs = reinterpret_cast<int4*>(smem + L::kSeqs);
   int* list = reinterpret_cast<int*>(smem + L::kList);
   const PromptOrder order = prompt_order(a, span, reinterpret_cast<int*>(smem + L::kSched), seqs,
                                          list, warp, lane);
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
-  const int wgroup = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 128, 0);
+  const int wgroup = warp >> 2;
 
   if (wgroup == 2) {
     regs_shrink<kPromptRegsOther>();
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (it.lim[t] == 0) continue;
       const int tok = it.tile_a + t * a.tile_tokens + row / G;    // this row's token
       const bool live = row < q_rows && tok < it.len;
-      const int lim = live ? tok + 1 : 0;
+      const int lim = live ? tok + 1 : it.nkb[t] * kPrefillKeys;   // (what a row of no token holds is not written)
       float m = -INFINITY, l = 0.f;
       const int nkb = it.nkb[t];
       for (int j = 0; j < nkb; ++j) {

@@ -69,7 +69,7 @@ struct PwSmem {
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kSched = kAbort + 4;
   static constexpr int kSeqs = (kSched + 128 + 15) & ~15;
-  static constexpr int kList = kSeqs + 8 * kPromptRankSeqs;
+  static constexpr int kList = kSeqs + 16 * kPromptRankSeqs;
   static constexpr int kBytes = kList + 4 * kPromptRankUnits;
   static constexpr int kAlloc = kBytes + 1024;        // one CTA per SM: both sizes pass 114 KB
   static_assert(kBytes > 114 * 1024, "one CTA holds all of an SM's tensor memory");
@@ -85,14 +85,14 @@ struct PwItem {
 // The pairs of a sequence are ranked as the attention's are (more keys, more
 // work); here the first keys are seen by most tokens.
 __device__ __forceinline__ void pw_item(const PromptWeightsArgs& a, const PromptOrder& o,
-                                        const int2* seqs, const int* list, int i, PwItem& it) {
+                                        const int4* seqs, const int* list, int i, PwItem& it) {
   const int u = i / a.num_kv_heads;
   it.kvh = i - u * a.num_kv_heads;
-  const int2 unit = prompt_unit(a, o, seqs, list, u, kPwSpan);
-  it.s = unit.x;
-  it.q0 = a.seq_starts[it.s];
-  it.len = a.seq_starts[it.s + 1] - it.q0;
-  it.k0 = ((it.len + kPwSpan - 1) / kPwSpan - 1 - unit.y) * kPwSpan;
+  const PromptUnit unit = prompt_unit(a, o, seqs, list, u, kPwSpan);
+  it.s = unit.s;
+  it.q0 = unit.q0;
+  it.len = unit.len;
+  it.k0 = ((it.len + kPwSpan - 1) / kPwSpan - 1 - unit.pair) * kPwSpan;
   it.t0 = max(it.k0, it.len - a.window);
   it.tiles = (it.len - it.t0 + a.tile_tokens - 1) / a.tile_tokens;
   it.blocks = min(kPwBlocks, (it.len - it.k0 + 127) / 128);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   pdl_wait();
 
   const int G = a.group;
-  int2* seqs = reinterpret_cast<int2*>(smem + L::kSeqs);
+  int4* seqs = reinterpret_cast<int4*>(smem + L::kSeqs);
   int* list = reinterpret_cast<int*>(smem + L::kList);
   const PromptOrder order = prompt_order(a, kPwSpan, reinterpret_cast<int*>(smem + L::kSched),
                                          seqs, list, warp, lane);
