@@ -121,7 +121,8 @@ __device__ __forceinline__ int warp_uniform(int x) { return __shfl_sync(0xffffff
 // special-function unit (16 results a cycle and SM) would bound: with n the
 // nearest integer of x, s = 2^n and p a polynomial of degree 5 for 2^(x - n),
 // the minimax fit of the relative error on [-1/2, 1/2] (7.5e-8, 2.1e-7 in fp32).
-// x is taken as at least -126 (2^-126 for less); a NaN stays one, +inf gives NaN.
+// Below -126.5 s is 0 (2^-127 has no exponent field), so a masked key's p is; a
+// NaN stays one, +inf gives NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -129,7 +130,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 __device__ __forceinline__ void exp2_fma(float2 x, float2& p, float2& s) {
   auto both = [](float v) { return make_float2(v, v); };
-  x = make_float2(max_nan(x.x, -126.f), max_nan(x.y, -126.f));
+  x = make_float2(max_nan(x.x, -127.f), max_nan(x.y, -127.f));
   const float2 t = ffma2(x, both(1.f), both(12582912.f));          // 1.5 * 2^23 + n
   const float2 f = ffma2(ffma2(t, both(1.f), both(-12582912.f)), both(-1.f), x);
   p = ffma2(f, both(0.0013276472454890609f), both(0.009675540961325169f));
@@ -347,7 +348,14 @@ __device__ __forceinline__ void prompt_softmax_block(float (&p)[kPrefillKeys], b
     for (int q = 0; q < 32; ++q) {
       const int c = 64 * half + 2 * q;
       const float2 x = ffma2(make_float2(p[c], p[c + 1]), mul2, neg);
-      const float2 e = make_float2(ex2(x.x), ex2(x.y));
+      float2 e;
+      if (q % 8 == 7) {   // one pair in eight on the FMA pipe (packed batch 306.5 -> 300.6 us)
+        float2 u, s;
+        exp2_fma(x, u, s);
+        e = fmul2(u, s);
+      } else {
+        e = make_float2(ex2(x.x), ex2(x.y));
+      }
       h[q] = pack2<BF16>(e.x, e.y);
       sum[q & 1] = ffma2(e, one, sum[q & 1]);
     }
