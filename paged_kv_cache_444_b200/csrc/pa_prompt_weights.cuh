@@ -11,25 +11,24 @@
 // over its columns in registers; nothing is shuffled, no sum leaves the thread
 // before it is written, and the order of the additions is fixed.
 //
-// Work item: (sequence, KV head, four blocks of 128 keys).  The item's K stays in
-// shared memory while the query tiles stream through a ring, each loaded once
-// for the four key blocks.  One consumer warpgroup a key block: it frees its S^T
-// as soon as that is in registers, so that the next tile's product runs during
-// the 2^x, and the four together keep four warps on each scheduler, which is what
-// bounds it (2^x takes 8 cycles of a scheduler's special-function unit for 32
-// elements; 3 of 8 run on the FMA pipe instead).  Warps: 0-15 the key blocks, 16
-// issues the MMAs, 17 the loads, 18 brings each tile's lse into shared memory
-// (negated, in log2 units).
+// Work item: (sequence, KV head, two blocks of 128 keys).  The item's K stays in
+// shared memory (two items' in flight) while the query tiles stream through a
+// ring, each loaded once for both key blocks.  Four consumer warpgroups: key block
+// b of the even tiles and of the odd ones, each with an S^T buffer of its own, so
+// that the next tile's product runs during this one's 2^x and the four warps of a
+// scheduler are at different places.  At the end of an item the two partial sums
+// of a key meet in shared memory.  Warps: 0-15 the sums, 16 issues the MMAs, 17
+// the loads, 18 brings each tile's lse into shared memory (negated, in log2 units).
 #pragma once
 
 #include "pa_prompt.cuh"
 
 namespace pa {
 
-constexpr int kPwBlocks = 4;                    // key blocks of an item
+constexpr int kPwBlocks = 2;                    // key blocks of an item
 constexpr int kPwSpan = 128 * kPwBlocks;        // keys of an item
-constexpr int kPwThreads = (4 * kPwBlocks + 3) * 32;
-constexpr int kPwWarpMma = 4 * kPwBlocks, kPwWarpTma = kPwWarpMma + 1, kPwWarpLse = kPwWarpMma + 2;
+constexpr int kPwThreads = 19 * 32;
+constexpr int kPwWarpMma = 16, kPwWarpTma = 17, kPwWarpLse = 18;
 
 struct PromptWeightsArgs {
   float* weights;              // [S, Hk, max_tokens]
@@ -51,26 +50,29 @@ struct PwSmem {
   static constexpr int kSlabs = D / 64;
   static constexpr int kSlab = 128 * 128;
   static constexpr int kTile = kSlabs * kSlab;        // one key block, or one query tile
+  static constexpr int NK = 2;                        // items' K in flight
   static constexpr int NQ = D == 64 ? 4 : 2;          // query tiles in flight
   static constexpr int NL = 4;                        // tiles' lse in flight
   static constexpr int kK = 0;
-  static constexpr int kQ = kK + kPwBlocks * kTile;
+  static constexpr int kQ = kK + NK * kPwBlocks * kTile;
   static constexpr int kLse = kQ + NQ * kTile;        // NL x 128 floats
-  static constexpr int kBarKFull = kLse + NL * 512;   // per key block
-  static constexpr int kBarKEmpty = kBarKFull + 8 * kPwBlocks;
-  static constexpr int kBarSFull = kBarKEmpty + 8 * kPwBlocks;
-  static constexpr int kBarSEmpty = kBarSFull + 8 * kPwBlocks;
-  static constexpr int kBarQFull = kBarSEmpty + 8 * kPwBlocks;
+  static constexpr int kBarKFull = kLse + NL * 512;
+  static constexpr int kBarKEmpty = kBarKFull + 8 * NK;
+  static constexpr int kBarSFull = kBarKEmpty + 8 * NK;    // [block][tile parity]
+  static constexpr int kBarSEmpty = kBarSFull + 8 * 4;
+  static constexpr int kBarQFull = kBarSEmpty + 8 * 4;
   static constexpr int kBarQEmpty = kBarQFull + 8 * NQ;
   static constexpr int kBarLFull = kBarQEmpty + 8 * NQ;
   static constexpr int kBarLEmpty = kBarLFull + 8 * NL;
-  static constexpr int kBarEnd = kBarLEmpty + 8 * NL;
+  static constexpr int kBarSums = kBarLEmpty + 8 * NL;     // an item's partial sums are in
+  static constexpr int kBarEnd = kBarSums + 8;
   static constexpr int kTmemSlot = kBarEnd + 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kSched = kAbort + 4;
   static constexpr int kSeqs = (kSched + 128 + 15) & ~15;
   static constexpr int kList = kSeqs + 16 * kPromptRankSeqs;
-  static constexpr int kBytes = kList + 4 * kPromptRankUnits;
+  static constexpr int kSums = kList + 4 * kPromptRankUnits;   // of two items: one float a key
+  static constexpr int kBytes = kSums + 2 * kPwSpan * 4;
   static constexpr int kAlloc = kBytes + 1024;        // one CTA per SM: both sizes pass 114 KB
   static_assert(kBytes > 114 * 1024, "one CTA holds all of an SM's tensor memory");
 };
@@ -153,19 +155,22 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kPwBlocks; ++i) {
+    for (int i = 0; i < L::NK; ++i) {
       mbar_init(sb + L::kBarKFull + 8 * i, 1);
       mbar_init(sb + L::kBarKEmpty + 8 * i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(sb + L::kBarSFull + 8 * i, 1);
       mbar_init(sb + L::kBarSEmpty + 8 * i, 128);
     }
+    mbar_init(sb + L::kBarSums, 512);
     for (int i = 0; i < L::NQ; ++i) {
       mbar_init(sb + L::kBarQFull + 8 * i, 1);
       mbar_init(sb + L::kBarQEmpty + 8 * i, 1);
     }
     for (int i = 0; i < L::NL; ++i) {
       mbar_init(sb + L::kBarLFull + 8 * i, 32);
-      mbar_init(sb + L::kBarLEmpty + 8 * i, 128 * kPwBlocks);
+      mbar_init(sb + L::kBarLEmpty + 8 * i, 256);
     }
     mbar_init(sb + L::kBarEnd, 1);
     *abort_flag = 0;
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   if (warp == kPwWarpMma) tmem_alloc(sb + L::kTmemSlot, kTmemCols);
   if (warp < kPwWarpMma && q_rows < 128) {   // rows no query box covers: finite (their lse is +inf)
     const int chunks = (128 - q_rows) * 8;
-    for (int i = threadIdx.x; i < chunks * L::kSlabs * L::NQ; i += 128 * kPwBlocks) {
+    for (int i = threadIdx.x; i < chunks * L::kSlabs * L::NQ; i += 512) {
       const int b = i / chunks, c = i % chunks;
       sts128(sb + L::kQ + b * L::kSlab + q_rows * 128 + c * 16, 0u, 0u, 0u, 0u);
     }
@@ -190,27 +195,26 @@ __global__ void __launch_bounds__(kPwThreads, 1)
 
   if (warp == kPwWarpTma) {
     // ================= loads =================
-    int nk[kPwBlocks] = {}, nq = 0;      // items so far with each key block, query tiles
+    int nk = 0, nq = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
       if (i < 0) break;
       PwItem it;
       pw_item(a, order, seqs, list, i, it);
-#pragma unroll
-      for (int b = 0; b < kPwBlocks; ++b) {
-        if (b >= it.blocks || !ok) continue;
-        if (nk[b] > 0 && !(ok = wait(sb + L::kBarKEmpty + 8 * b, (nk[b] - 1) & 1))) continue;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(sb + L::kBarKFull + 8 * b, L::kTile);
+      const int ks = nk % L::NK;
+      if (nk >= L::NK && !(ok = wait(sb + L::kBarKEmpty + 8 * ks, ((nk / L::NK) & 1) ^ 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(sb + L::kBarKFull + 8 * ks, it.blocks * L::kTile);
+        for (int b = 0; b < it.blocks; ++b) {
 #pragma unroll
           for (int c = 0; c < L::kSlabs; ++c)
-            tma_load_4d(sb + L::kK + b * L::kTile + c * L::kSlab, &kmap,
-                        sb + L::kBarKFull + 8 * b, 0, c, it.kvh, it.q0 + it.k0 + 128 * b);
+            tma_load_4d(sb + L::kK + (ks * kPwBlocks + b) * L::kTile + c * L::kSlab, &kmap,
+                        sb + L::kBarKFull + 8 * ks, 0, c, it.kvh, it.q0 + it.k0 + 128 * b);
         }
-        __syncwarp();
-        ++nk[b];
       }
+      __syncwarp();
+      ++nk;
       for (int j = 0; j < it.tiles && ok; ++j) {
         const int qs = nq % L::NQ;
         if (nq >= L::NQ && !(ok = wait(sb + L::kBarQEmpty + 8 * qs, ((nq / L::NQ) & 1) ^ 1))) break;
@@ -227,9 +231,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
     }
     // every load issued lands before the CTA can exit
-#pragma unroll
-    for (int b = 0; b < kPwBlocks; ++b)
-      if (nk[b] > 0) mbar_wait_bounded(sb + L::kBarKFull + 8 * b, (nk[b] - 1) & 1);
+    for (int g = max(0, nk - L::NK); g < nk; ++g)
+      mbar_wait_bounded(sb + L::kBarKFull + 8 * (g % L::NK), (g / L::NK) & 1);
     for (int g = max(0, nq - L::NQ); g < nq; ++g)
       mbar_wait_bounded(sb + L::kBarQFull + 8 * (g % L::NQ), (g / L::NQ) & 1);
   } else if (warp == kPwWarpMma) {
@@ -239,45 +242,48 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     const uint64_t kdesc = umma_desc_sw128(sb + L::kK, 16, 1024);
     const uint64_t qdesc = umma_desc_sw128(sb + L::kQ, 16, 1024);
     const bool leader = elect_lane();
-    int nk[kPwBlocks] = {}, ns[kPwBlocks] = {}, nq = 0;
+    int nk = 0, nq = 0, ns = 0;          // ns: bit 2 b + h the phase of that S buffer
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
       if (i < 0) break;
       PwItem it;
       pw_item(a, order, seqs, list, i, it);
-      const int tiles = warp_uniform(it.tiles), blocks = warp_uniform(it.blocks);
-      int first[kPwBlocks];
-#pragma unroll
-      for (int b = 0; b < kPwBlocks; ++b) first[b] = warp_uniform(pw_first(it, a.tile_tokens, b));
+      const int tiles = warp_uniform(it.tiles);
+      const int first1 = warp_uniform(it.blocks > 1 ? pw_first(it, a.tile_tokens, 1) : it.tiles);
+      const int ks = nk % L::NK;
+      if (!(ok = wait(sb + L::kBarKFull + 8 * ks, (nk / L::NK) & 1))) break;
       for (int j = 0; j < tiles && ok; ++j, ++nq) {
-        const int qs = nq % L::NQ;
+        const int qs = nq % L::NQ, h = nq & 1;
         if (!(ok = wait(sb + L::kBarQFull + 8 * qs, (nq / L::NQ) & 1))) break;
 #pragma unroll
         for (int b = 0; b < kPwBlocks; ++b) {
-          if (b >= blocks || j < first[b] || !ok) continue;
-          if (j == first[b] && !(ok = wait(sb + L::kBarKFull + 8 * b, nk[b] & 1))) continue;
-          if (ns[b] > 0 && !(ok = wait(sb + L::kBarSEmpty + 8 * b, (ns[b] - 1) & 1))) continue;
+          if ((b == 1 && j < first1) || !ok) continue;
+          const int buf = 2 * b + h;
+          // (the phase before the first completes at once: a fresh barrier's)
+          if (!(ok = wait(sb + L::kBarSEmpty + 8 * buf, ((ns >> buf) & 1) ^ 1))) continue;
           tmem_fence_after_sync();
           if (leader) {
-            const uint64_t kd = kdesc + b * (L::kTile / 16), qd = qdesc + qs * (L::kTile / 16);
+            const uint64_t kd = kdesc + (ks * kPwBlocks + b) * (L::kTile / 16);
+            const uint64_t qd = qdesc + qs * (L::kTile / 16);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) / 16;
-              umma_f16_ss(tm + 128 * b, kd + off, qd + off, kId, kk > 0 ? 1u : 0u);
+              umma_f16_ss(tm + 128 * buf, kd + off, qd + off, kId, kk > 0 ? 1u : 0u);
             }
-            umma_commit(sb + L::kBarSFull + 8 * b);
-            if (j == tiles - 1) umma_commit(sb + L::kBarKEmpty + 8 * b);
+            umma_commit(sb + L::kBarSFull + 8 * buf);
           }
           __syncwarp();
-          ++ns[b];
+          ns ^= 1 << buf;
         }
         if (!ok) break;
-        if (leader) umma_commit(sb + L::kBarQEmpty + 8 * qs);
+        if (leader) {
+          umma_commit(sb + L::kBarQEmpty + 8 * qs);
+          if (j == tiles - 1) umma_commit(sb + L::kBarKEmpty + 8 * ks);
+        }
         __syncwarp();
       }
-#pragma unroll
-      for (int b = 0; b < kPwBlocks; ++b) nk[b] += b < blocks;
+      ++nk;
     }
     if (leader) umma_commit(sb + L::kBarEnd);
     __syncwarp();
@@ -312,11 +318,15 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
     }
   } else {
-    // ================= key block b, key = tensor-memory lane =================
-    const int b = warp >> 2, key = threadIdx.x & 127;
-    const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 * b;
+    // ================= key block b, tiles of parity h, key = tensor-memory lane ==========
+    const int b = (warp >> 2) & 1, h = warp >> 3, key = threadIdx.x & 127;
+    const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                            128 * (2 * b + h);
+    const uint32_t full = sb + L::kBarSFull + 8 * (2 * b + h);
+    const uint32_t empty = sb + L::kBarSEmpty + 8 * (2 * b + h);
     const float2 scale = make_float2(a.scale_log2, a.scale_log2);
-    int n = 0, ns = 0;
+    float* sums = reinterpret_cast<float*>(smem + L::kSums);
+    int n = 0, ns = 0, items = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
@@ -326,11 +336,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       const int kb = it.k0 + 128 * b, kj = kb + key;
       const int first = b < it.blocks ? pw_first(it, a.tile_tokens, b) : it.tiles;
       float acc = 0.f;
-      for (int j = 0; j < it.tiles; ++j, ++n) {
-        const int sl = n % L::NL;
-        if (!(ok = wait(sb + L::kBarLFull + 8 * sl, (n / L::NL) & 1))) break;
+      for (int j = (n & 1) ^ h; j < it.tiles; j += 2) {    // tile n + j has parity h
+        const int sl = (n + j) % L::NL;
+        if (!(ok = wait(sb + L::kBarLFull + 8 * sl, ((n + j) / L::NL) & 1))) break;
         if (j >= first) {
-          if (!(ok = wait(sb + L::kBarSFull + 8 * b, ns & 1))) break;
+          if (!(ok = wait(full, ns & 1))) break;
           tmem_fence_after_sync();
           const int tok0 = it.t0 + j * a.tile_tokens;
           const int rows = min(a.tile_tokens, it.len - tok0) * G;
@@ -339,36 +349,36 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           if (rows == q_rows && tok0 >= kb + 127) {
             // every column counts (those past q_rows have an lse of +inf)
 #pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
+            for (int c = 0; c < 4; ++c) {
               float u[32];
-              tmem_ld32(s_addr + 32 * h, u);
-              if (h == 3) {
+              tmem_ld32(s_addr + 32 * c, u);
+              if (c == 3) {
                 tmem_fence_before_sync();
-                mbar_arrive(sb + L::kBarSEmpty + 8 * b);   // S is in registers
+                mbar_arrive(empty);                    // S is in registers
               }
-              add_columns(u, lse4 + 8 * h, scale, sum);
+              add_columns(u, lse4 + 8 * c, scale, sum);
             }
           } else {
             // columns of tokens before this key, or past the tile's rows, do not count
             const int c0 = max(0, kj - tok0) * G;
 #pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
+            for (int g = 0; g < 4; ++g) {
               float s[32];
-              tmem_ld32(s_addr + 32 * h, s);
+              tmem_ld32(s_addr + 32 * g, s);
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const float4 neg = lse4[8 * h + q];
+                const float4 neg = lse4[8 * g + q];
                 const float n4[4] = {neg.x, neg.y, neg.z, neg.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const int c = 32 * h + 4 * q + e;
+                  const int c = 32 * g + 4 * q + e;
                   const float v = ex2(s[4 * q + e] * a.scale_log2 + n4[e]);
                   sum[e & 1].x += c >= c0 && c < rows ? v : 0.f;
                 }
               }
             }
             tmem_fence_before_sync();
-            mbar_arrive(sb + L::kBarSEmpty + 8 * b);
+            mbar_arrive(empty);
           }
           acc += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           ++ns;
@@ -376,10 +386,21 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         mbar_arrive(sb + L::kBarLEmpty + 8 * sl);
       }
       if (!ok) break;
+      n += it.tiles;
+      // the odd tiles' sums go to the even tiles' warpgroup.  Two items' sums
+      // alternate: a thread that writes those of the item after next has passed
+      // the barrier of the next one, which every reader of this one's reaches later.
+      float* part = sums + (items & 1) * kPwSpan;
+      if (h == 1) part[128 * b + key] = acc;
+      mbar_arrive(sb + L::kBarSums);
+      if (!(ok = wait(sb + L::kBarSums, items & 1))) break;
+      ++items;
+      if (h == 1) continue;
       if (it.len > a.max_tokens) {
         if (key == 0 && b == 0 && it.k0 == 0 && it.kvh == 0) record_error(kErrContextLen, it.s);
       } else if (kj < it.len && b < it.blocks) {
-        a.weights[(static_cast<size_t>(it.s) * a.num_kv_heads + it.kvh) * a.max_tokens + kj] = acc;
+        a.weights[(static_cast<size_t>(it.s) * a.num_kv_heads + it.kvh) * a.max_tokens + kj] =
+            acc + part[128 * b + key];
       }
     }
   }
