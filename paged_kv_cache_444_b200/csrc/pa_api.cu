@@ -1409,7 +1409,7 @@ extern "C" pa_status pa_decode_weights(void* out, float* weights, void* workspac
   if (workspace_bytes < l.total) return PA_ERR_SHAPE;
   const int64_t runs = (max_blocks_per_seq * block_size + kWeightsRun - 1) / kWeightsRun;
   const int64_t items = num_seqs * num_kv_heads * l.parts;
-  const int64_t merge = num_seqs * num_heads + num_seqs * num_kv_heads * runs;
+  const int64_t merge = num_seqs * num_kv_heads * runs;
   if (items > INT32_MAX || merge > INT32_MAX) return PA_ERR_SHAPE;
   CUtensorMap km, vm;
   if (!encode_cache_map(&km, key_cache, dtype, num_blocks, num_kv_heads, head_dim) ||

@@ -13,9 +13,13 @@
 //     kWeightsPart tokens): the page pipeline and the transposed page step of
 //     the split decode (tokens and head dims as the mma's rows, heads as its
 //     columns, one or two column tiles of 8), with the logits written out.
-//   weights_merge_kernel  S x H CTAs merge the partitions' O by log-sum-exp;
-//     the others take a run of tokens each, find the heads' lse from the
-//     partitions' maxima and sums, and add the weights up.
+//   weights_merge_kernel  a CTA per (sequence, KV head, run of tokens) finds the
+//     heads' lse from the partitions' maxima and sums, adds the weights of its
+//     run up, and merges a share of the heads' output columns.
+//
+// Both passes are bound by HBM.  K and V are loaded evict-first, so that the
+// logits, small enough for L2 (16 bytes a token at G = 4), are still there when
+// the second pass reads them.
 #pragma once
 
 #include "pa_decode.cuh"
@@ -23,9 +27,9 @@
 namespace pa {
 
 constexpr int kWeightsPart = 512;          // tokens per partition
-constexpr int kWeightsRun = 1024;          // tokens per CTA of the second pass
+constexpr int kWeightsRun = 2048;          // tokens per CTA of the second pass
 constexpr int kWeightsThreads = 256;
-constexpr int kWeightsBatch = 8;           // partitions of O loaded before any is used
+constexpr int kWeightsBatch = 4;           // tokens (or partitions of O) loaded before any is used
 
 struct WeightsArgs {
   const uint16_t* query;         // [S, H, D]
@@ -49,6 +53,21 @@ struct WeightsArgs {
   int parts;                     // P
   int runs;                      // CTAs per (sequence, KV head) that add weights up
 };
+
+// tma_load_4d for data read once: first to leave L2.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_load_4d_once(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                 int c0, int c1, int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
+      : "memory");
+}
 
 // ---------------------------------------------------------------------------
 // Per-warp state and page step: S^T = K Q^T, O^T = V^T P^T for NT tiles of 8
@@ -261,6 +280,7 @@ __global__ void __launch_bounds__(kThreads)
       id = -1;   // a box at a negative row reads zeros
     }
   }
+  const uint64_t once = evict_first_policy();
   auto issue = [&](int k) {   // whole warp; lane 0 loads this warp's page k
     const int row = __shfl_sync(0xffffffffu, id, warp + k * kWarps) * kPage;
     if (lane == 0) {
@@ -269,10 +289,10 @@ __global__ void __launch_bounds__(kThreads)
       mbar_arrive_expect_tx(bar, L::kStageBytes);
 #pragma unroll
       for (int b = 0; b < L::kBoxesPerRow; ++b)
-        tma_load_4d(dk + b * kBoxBytes, &kmap, bar, 0, b, kvh, row);
+        tma_load_4d_once(dk + b * kBoxBytes, &kmap, bar, 0, b, kvh, row, once);
 #pragma unroll
       for (int b = 0; b < L::kBoxesPerRow; ++b)
-        tma_load_4d(dv + b * kBoxBytes, &vmap, bar, 0, b, kvh, row);
+        tma_load_4d_once(dv + b * kBoxBytes, &vmap, bar, 0, b, kvh, row, once);
     }
   };
   for (int k = 0; k < min(my_pages, NST); ++k) issue(k);
@@ -342,99 +362,114 @@ __device__ __forceinline__ float warp_lse(const float* m, const float* l, int np
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kWeightsThreads)
     weights_merge_kernel(const WeightsArgs a) {
-  __shared__ float4 acc_sh[kWeightsThreads];
-  __shared__ float lse_sh[kWeightsThreads / 32 * 2];
+  constexpr int kWarpsM = kWeightsThreads / 32;
+  __shared__ float part_sh[kWarpsM][32];
+  __shared__ float lse_sh[16];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = a.max_blocks_per_seq * kPage;
-  const int rows = a.num_seqs * a.num_heads;
-  int b = blockIdx.x;
-  if (b < rows) {
-    // ---- O of one (sequence, head) ----
-    const int ctx = min(max(a.context_lens[b / a.num_heads], 0), cap);
-    const int np = (ctx + kWeightsPart - 1) / kWeightsPart;
-    const size_t base = static_cast<size_t>(b) * a.parts;
-    if (warp == 0) {
-      const float lse = warp_lse(a.part_m + base, a.part_l + base, np, lane);
-      if (lane == 0) lse_sh[0] = lse;
-    }
-    __syncthreads();
-    const float lse = lse_sh[0];
-    constexpr int kQuads = D / 4, kGroups = kWeightsThreads / kQuads;
-    const int q = tid % kQuads, grp = tid / kQuads;
-    const float4* src = reinterpret_cast<const float4*>(a.tmp_out + base * D) + q;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = grp; p0 < np; p0 += kGroups * kWeightsBatch) {
-      float4 v[kWeightsBatch];
-      float f[kWeightsBatch];
-#pragma unroll
-      for (int u = 0; u < kWeightsBatch; ++u) {
-        const int p = p0 + u * kGroups;
-        f[u] = p < np ? a.part_m[base + p] : -INFINITY;
-        v[u] = p < np ? src[static_cast<size_t>(p) * kQuads] : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int u = 0; u < kWeightsBatch; ++u) {
-        const float e = ex2(f[u] - lse);
-        acc.x += e * v[u].x;
-        acc.y += e * v[u].y;
-        acc.z += e * v[u].z;
-        acc.w += e * v[u].w;
-      }
-    }
-    acc_sh[tid] = acc;
-    __syncthreads();
-    if (tid < kQuads) {
-      for (int g = 1; g < kGroups; ++g) {
-        const float4 u = acc_sh[g * kQuads + tid];
-        acc.x += u.x;
-        acc.y += u.y;
-        acc.z += u.z;
-        acc.w += u.w;
-      }
-      uint2 r;
-      r.x = pack2<BF16>(acc.x, acc.y);
-      r.y = pack2<BF16>(acc.z, acc.w);
-      *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(b) * D + tid * 4) = r;
-    }
-    return;
-  }
-  // ---- the weights of a run of tokens ----
-  b -= rows;
-  const int run = b % a.runs, row = b / a.runs;        // row = s * Hk + kv
+  const int run = blockIdx.x % a.runs, row = blockIdx.x / a.runs;   // row = s * Hk + kv
   const int s = row / a.num_kv_heads, kv = row % a.num_kv_heads;
   const int ctx = min(max(a.context_lens[s], 0), cap);
-  if (ctx > a.max_tokens) {
-    if (tid == 0 && run == 0 && kv == 0) record_error(kErrContextLen, s);
-    return;
-  }
   const int t0 = run * kWeightsRun, t1 = min(t0 + kWeightsRun, ctx);
-  if (t0 >= t1) return;
+  if (t0 >= t1 && run > 0) return;
   const int np = (ctx + kWeightsPart - 1) / kWeightsPart;
   const int G = a.group;
-  for (int g = warp; g < G; g += kWeightsThreads / 32) {
-    const size_t base = (static_cast<size_t>(s) * a.num_heads + kv * G + g) * a.parts;
+  const size_t hrow = static_cast<size_t>(s) * a.num_heads + kv * G;
+  for (int g = warp; g < G; g += kWarpsM) {
+    const size_t base = (hrow + g) * a.parts;
     const float lse = warp_lse(a.part_m + base, a.part_l + base, np, lane);
     if (lane == 0) lse_sh[g] = lse;
   }
   __syncthreads();
-  const float* z = a.logits + static_cast<size_t>(row) * cap * G;
-  float* w = a.weights + static_cast<size_t>(row) * a.max_tokens;
-  const int fresh = max(ctx - a.new_tokens, 0);        // tokens from here on start anew
-  for (int t = t0 + tid; t < t1; t += kWeightsThreads) {
-    const float* zt = z + static_cast<size_t>(t) * G;
-    float sum = 0.f;
-    if ((G & 3) == 0) {
-      for (int g = 0; g < G; g += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(zt + g);
-        sum += (ex2(v.x - lse_sh[g]) + ex2(v.y - lse_sh[g + 1])) +
-               (ex2(v.z - lse_sh[g + 2]) + ex2(v.w - lse_sh[g + 3]));
+
+  // ---- the weights of the run ----
+  if (ctx > a.max_tokens) {
+    if (tid == 0 && run == 0 && kv == 0) record_error(kErrContextLen, s);
+  } else {
+    const float* z = a.logits + static_cast<size_t>(row) * cap * G;
+    float* w = a.weights + static_cast<size_t>(row) * a.max_tokens;
+    const int fresh = max(ctx - a.new_tokens, 0);      // tokens from here on start anew
+    for (int b0 = t0; b0 < t1; b0 += kWeightsThreads * kWeightsBatch) {
+      float sum[kWeightsBatch], old[kWeightsBatch];
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) {
+        const int t = b0 + u * kWeightsThreads + tid;
+        old[u] = t < min(t1, fresh) ? w[t] : 0.f;
+        sum[u] = 0.f;
       }
-    } else {
-      for (int g = 0; g < G; ++g) sum += ex2(zt[g] - lse_sh[g]);
+      if ((G & 3) == 0) {
+        for (int g = 0; g < G; g += 4) {
+          float4 v[kWeightsBatch];
+#pragma unroll
+          for (int u = 0; u < kWeightsBatch; ++u) {
+            const int t = b0 + u * kWeightsThreads + tid;
+            v[u] = t < t1 ? *reinterpret_cast<const float4*>(z + static_cast<size_t>(t) * G + g)
+                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          }
+#pragma unroll
+          for (int u = 0; u < kWeightsBatch; ++u)
+            sum[u] += (ex2(v[u].x - lse_sh[g]) + ex2(v[u].y - lse_sh[g + 1])) +
+                      (ex2(v[u].z - lse_sh[g + 2]) + ex2(v[u].w - lse_sh[g + 3]));
+        }
+      } else {
+        for (int g = 0; g < G; ++g) {
+          float v[kWeightsBatch];
+#pragma unroll
+          for (int u = 0; u < kWeightsBatch; ++u) {
+            const int t = b0 + u * kWeightsThreads + tid;
+            v[u] = t < t1 ? z[static_cast<size_t>(t) * G + g] : -INFINITY;
+          }
+#pragma unroll
+          for (int u = 0; u < kWeightsBatch; ++u) sum[u] += ex2(v[u] - lse_sh[g]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) {
+        const int t = b0 + u * kWeightsThreads + tid;
+        if (t < t1) w[t] = t < fresh ? old[u] + sum[u] : sum[u];
+      }
     }
-    w[t] = t < fresh ? w[t] + sum : sum;
+  }
+
+  // ---- this run's share of the heads' output columns, 32 at a time ----
+  const int live_runs = max(1, (ctx + kWeightsRun - 1) / kWeightsRun);
+  const int units = G * D / 32, per = (units + live_runs - 1) / live_runs;
+  const int u0 = min(run * per, units), u1 = min(u0 + per, units);
+  // a unit's partitions over `share` warps, so that few units keep all warps busy
+  const int share = u1 - u0 >= kWarpsM ? 1 : u1 - u0 >= 4 ? 2 : u1 - u0 >= 2 ? 4 : 8;
+  for (int ub = u0; ub < u1; ub += kWarpsM / share) {
+    const int u = ub + warp / share, first = warp % share;
+    float acc = 0.f;
+    if (u < u1) {
+      const int g = u / (D / 32), col = u % (D / 32) * 32 + lane;
+      const size_t base = (hrow + g) * a.parts;
+      const float lse = lse_sh[g];
+      for (int p0 = first; p0 < np; p0 += share * kWeightsBatch) {
+        float v[kWeightsBatch], m[kWeightsBatch];
+#pragma unroll
+        for (int i = 0; i < kWeightsBatch; ++i) {
+          const int p = p0 + i * share;
+          m[i] = p < np ? a.part_m[base + p] : -INFINITY;
+          v[i] = p < np ? a.tmp_out[(base + p) * D + col] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kWeightsBatch; ++i) acc += ex2(m[i] - lse) * v[i];
+      }
+    }
+    if (share > 1) {
+      __syncthreads();
+      part_sh[warp][lane] = acc;
+      __syncthreads();
+      for (int i = 1; i < share && first == 0; ++i) acc += part_sh[warp + i][lane];
+    }
+    // two columns a store
+    const float hi = __shfl_down_sync(0xffffffffu, acc, 1);
+    if (u < u1 && first == 0 && !(lane & 1)) {
+      const int g = u / (D / 32), col = u % (D / 32) * 32 + lane;
+      *reinterpret_cast<uint32_t*>(a.out + (hrow + g) * D + col) = pack2<BF16>(acc, hi);
+    }
   }
 }
 
