@@ -17,9 +17,14 @@
 //     heads' lse from the partitions' maxima and sums, adds the weights of its
 //     run up, and merges a share of the heads' output columns.
 //
-// Both passes are bound by HBM.  K and V are loaded evict-first, so that the
+// The first pass is bound by HBM (128 sequences of 512 to 4096 tokens, 32/8 heads:
+// 193 us for 1.26 GB, 6.5 TB/s).  K and V are loaded evict-first, so that the
 // logits, small enough for L2 (16 bytes a token at G = 4), are still there when
-// the second pass reads them.
+// the second pass reads them: it reads 4 MB of its 58 from DRAM, and costs the
+// call another 20 us, most of it latency at the first pass's end (with a CTA a
+// row of outputs and 1024 tokens a CTA the two took 234 us, now 214; with 512
+// threads, or 1024 or 2048 tokens, 216 to 221).  8 sequences of 32768 to 131072
+// tokens: 460 us, the second pass 35 of them.
 #pragma once
 
 #include "pa_decode.cuh"
@@ -27,7 +32,7 @@
 namespace pa {
 
 constexpr int kWeightsPart = 512;          // tokens per partition
-constexpr int kWeightsRun = 2048;          // tokens per CTA of the second pass
+constexpr int kWeightsRun = 4096;          // tokens per CTA of the second pass
 constexpr int kWeightsThreads = 256;
 constexpr int kWeightsBatch = 4;           // tokens (or partitions of O) loaded before any is used
 
@@ -363,8 +368,8 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kWeightsThreads)
     weights_merge_kernel(const WeightsArgs a) {
   constexpr int kWarpsM = kWeightsThreads / 32;
-  __shared__ float part_sh[kWarpsM][32];
-  __shared__ float lse_sh[16];
+  __shared__ float part_sh[kWarpsM][D / 32][32];
+  __shared__ __align__(16) float lse_sh[16];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -391,84 +396,105 @@ __global__ void __launch_bounds__(kWeightsThreads)
     const float* z = a.logits + static_cast<size_t>(row) * cap * G;
     float* w = a.weights + static_cast<size_t>(row) * a.max_tokens;
     const int fresh = max(ctx - a.new_tokens, 0);      // tokens from here on start anew
-    for (int b0 = t0; b0 < t1; b0 += kWeightsThreads * kWeightsBatch) {
-      float sum[kWeightsBatch], old[kWeightsBatch];
+    constexpr int kStep = kWeightsThreads * kWeightsBatch;
+    for (int b0 = t0; b0 < t1; b0 += kStep) {
+      // whole batches of tokens that are not new need no checks, and take four
+      // heads a load
+      if ((G & 3) == 0 && b0 + kStep <= min(t1, fresh)) {
+        const float4* zt = reinterpret_cast<const float4*>(z + static_cast<size_t>(b0 + tid) * G);
+        float* wt = w + b0 + tid;
+        float sum[kWeightsBatch];
 #pragma unroll
-      for (int u = 0; u < kWeightsBatch; ++u) {
-        const int t = b0 + u * kWeightsThreads + tid;
-        old[u] = t < min(t1, fresh) ? w[t] : 0.f;
-        sum[u] = 0.f;
-      }
-      if ((G & 3) == 0) {
+        for (int u = 0; u < kWeightsBatch; ++u) sum[u] = wt[u * kWeightsThreads];
         for (int g = 0; g < G; g += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(lse_sh + g);
           float4 v[kWeightsBatch];
 #pragma unroll
-          for (int u = 0; u < kWeightsBatch; ++u) {
-            const int t = b0 + u * kWeightsThreads + tid;
-            v[u] = t < t1 ? *reinterpret_cast<const float4*>(z + static_cast<size_t>(t) * G + g)
-                          : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          }
+          for (int u = 0; u < kWeightsBatch; ++u)
+            v[u] = zt[(u * kWeightsThreads * G + g) >> 2];
 #pragma unroll
           for (int u = 0; u < kWeightsBatch; ++u)
-            sum[u] += (ex2(v[u].x - lse_sh[g]) + ex2(v[u].y - lse_sh[g + 1])) +
-                      (ex2(v[u].z - lse_sh[g + 2]) + ex2(v[u].w - lse_sh[g + 3]));
+            sum[u] += (ex2(v[u].x - l.x) + ex2(v[u].y - l.y)) +
+                      (ex2(v[u].z - l.z) + ex2(v[u].w - l.w));
         }
-      } else {
-        for (int g = 0; g < G; ++g) {
-          float v[kWeightsBatch];
 #pragma unroll
-          for (int u = 0; u < kWeightsBatch; ++u) {
-            const int t = b0 + u * kWeightsThreads + tid;
-            v[u] = t < t1 ? z[static_cast<size_t>(t) * G + g] : -INFINITY;
-          }
+        for (int u = 0; u < kWeightsBatch; ++u) wt[u * kWeightsThreads] = sum[u];
+        continue;
+      }
+      float sum[kWeightsBatch] = {};
+      for (int g = 0; g < G; ++g) {
+        float v[kWeightsBatch];
 #pragma unroll
-          for (int u = 0; u < kWeightsBatch; ++u) sum[u] += ex2(v[u] - lse_sh[g]);
+        for (int u = 0; u < kWeightsBatch; ++u) {
+          const int t = b0 + u * kWeightsThreads + tid;
+          v[u] = t < t1 ? z[static_cast<size_t>(t) * G + g] : -INFINITY;
         }
+#pragma unroll
+        for (int u = 0; u < kWeightsBatch; ++u) sum[u] += ex2(v[u] - lse_sh[g]);
       }
 #pragma unroll
       for (int u = 0; u < kWeightsBatch; ++u) {
         const int t = b0 + u * kWeightsThreads + tid;
-        if (t < t1) w[t] = t < fresh ? old[u] + sum[u] : sum[u];
+        if (t < t1) w[t] = t < fresh ? w[t] + sum[u] : sum[u];
       }
     }
   }
 
-  // ---- this run's share of the heads' output columns, 32 at a time ----
+  // ---- this run's share of the heads' outputs, a row a warp or several ----
   const int live_runs = max(1, (ctx + kWeightsRun - 1) / kWeightsRun);
-  const int units = G * D / 32, per = (units + live_runs - 1) / live_runs;
-  const int u0 = min(run * per, units), u1 = min(u0 + per, units);
-  // a unit's partitions over `share` warps, so that few units keep all warps busy
-  const int share = u1 - u0 >= kWarpsM ? 1 : u1 - u0 >= 4 ? 2 : u1 - u0 >= 2 ? 4 : 8;
-  for (int ub = u0; ub < u1; ub += kWarpsM / share) {
-    const int u = ub + warp / share, first = warp % share;
-    float acc = 0.f;
-    if (u < u1) {
-      const int g = u / (D / 32), col = u % (D / 32) * 32 + lane;
+  const int per = (G + live_runs - 1) / live_runs;
+  const int g0 = min(run * per, G), g1 = min(g0 + per, G);
+  // a row's partitions over `share` warps, so that few rows keep all warps busy
+  const int share = np < 2 || g1 - g0 >= kWarpsM ? 1 : g1 - g0 >= 4 ? 2 : g1 - g0 >= 2 ? 4 : 8;
+  constexpr int kVec = D / 32;                         // columns of a lane
+  for (int gb = g0; gb < g1; gb += kWarpsM / share) {
+    const int g = gb + warp / share, first = warp % share;
+    float acc[kVec] = {};
+    if (g < g1) {
       const size_t base = (hrow + g) * a.parts;
       const float lse = lse_sh[g];
       for (int p0 = first; p0 < np; p0 += share * kWeightsBatch) {
-        float v[kWeightsBatch], m[kWeightsBatch];
+        float v[kWeightsBatch][kVec], m[kWeightsBatch];
 #pragma unroll
         for (int i = 0; i < kWeightsBatch; ++i) {
           const int p = p0 + i * share;
-          m[i] = p < np ? a.part_m[base + p] : -INFINITY;
-          v[i] = p < np ? a.tmp_out[(base + p) * D + col] : 0.f;
+          m[i] = -INFINITY;
+          if (p < np) {
+            m[i] = a.part_m[base + p];
+            const float* src = a.tmp_out + (base + p) * D + lane * kVec;
+            if constexpr (kVec == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              v[i][0] = x.x; v[i][1] = x.y;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) v[i][c] = 0.f;
+          }
         }
 #pragma unroll
-        for (int i = 0; i < kWeightsBatch; ++i) acc += ex2(m[i] - lse) * v[i];
+        for (int i = 0; i < kWeightsBatch; ++i) {
+          const float e = ex2(m[i] - lse);
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) acc[c] += e * v[i][c];
+        }
       }
     }
     if (share > 1) {
       __syncthreads();
-      part_sh[warp][lane] = acc;
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) part_sh[warp][c][lane] = acc[c];
       __syncthreads();
-      for (int i = 1; i < share && first == 0; ++i) acc += part_sh[warp + i][lane];
+      for (int i = 1; i < share && first == 0; ++i)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) acc[c] += part_sh[warp + i][c][lane];
     }
-    // two columns a store
-    const float hi = __shfl_down_sync(0xffffffffu, acc, 1);
-    if (u < u1 && first == 0 && !(lane & 1)) {
-      const int g = u / (D / 32), col = u % (D / 32) * 32 + lane;
-      *reinterpret_cast<uint32_t*>(a.out + (hrow + g) * D + col) = pack2<BF16>(acc, hi);
+    if (g < g1 && first == 0) {
+      uint32_t* o = reinterpret_cast<uint32_t*>(a.out + (hrow + g) * D + lane * kVec);
+#pragma unroll
+      for (int c = 0; c < kVec; c += 2) o[c / 2] = pack2<BF16>(acc[c], acc[c + 1]);
     }
   }
 }
