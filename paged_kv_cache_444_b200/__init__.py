@@ -22,7 +22,7 @@ __all__ = [
     "pa_copy_blocks", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_split_fp8",
     "pa_prefill", "pa_prompt_attention", "pa_prompt_weights", "pa_decode_weights",
     "pa_evict_select", "pa_evict_compact", "pa_selftest_wait_timeout", "SplitWorkspace", "WeightsWorkspace",
-    "decode_step", "HostStep", "DecodePlan",
+    "EvictionState", "decode_step", "prompt_step", "HostStep", "DecodePlan",
 ]
 
 
@@ -87,3 +87,56 @@ def decode_step(query, key, value, key_cache, value_cache, slot_mapping, block_t
     else:
         pa_decode(out, query, key_cache, value_cache, block_tables, context_lens, scale, stream)
     return out
+
+
+def prompt_step(query, key, value, key_cache, value_cache, slot_mapping, seq_starts, scale: float,
+                out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                weights: torch.Tensor | None = None, window: int = 0, stream=None) -> torch.Tensor:
+    """The first step of packed prompts in one attention layer: write their K/V
+    rows into the cache (pa_reshape_and_cache; key_cache None: no write), attend
+    (pa_prompt_attention) and, when weights [S, Hk, max_tokens] is given, set the
+    attention weight each token receives from the last `window` tokens of its
+    prompt (pa_prompt_weights).  All tensors live on one CUDA device."""
+    T, H, _ = query.shape
+    if out is None:
+        out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+    if weights is not None and lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=query.device)
+    if key_cache is not None:
+        pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, stream)
+    pa_prompt_attention(out, lse, query, key, value, seq_starts, scale, stream)
+    if weights is not None:
+        pa_prompt_weights(weights, query, key, lse, seq_starts, scale, window, stream)
+    return out
+
+
+class EvictionState:
+    """What one attention layer keeps to hold its sequences to `budget` cached
+    tokens: the attention weight each slot's token has received (filled by
+    pa_prompt_weights and pa_decode_weights), the tokens' positions, and the
+    buffers of pa_evict_select.  The first `sink` tokens of a sequence and its
+    latest `recent` ones always stay.  For a new sequence in row s, set
+    recorded_lens[s] to 0."""
+
+    def __init__(self, num_seqs: int, num_kv_heads: int, max_tokens: int, budget: int,
+                 device: torch.device | str, sink: int = 4, recent: int = 0):
+        rows = (num_seqs, num_kv_heads)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.sink, self.recent = int(sink), int(recent)
+        self.weights = torch.zeros(rows + (max_tokens,), dtype=torch.float32, device=device)
+        self.positions = torch.zeros(rows + (max_tokens,), **i32)
+        self.recorded_lens = torch.zeros(num_seqs, **i32)
+        self.source = torch.empty(rows + (budget,), **i32)
+        self.new_lens = torch.empty(num_seqs, **i32)
+
+    def evict(self, key_cache, value_cache, block_tables, context_lens, seq_lens) -> None:
+        """Evict down to the budget on the current stream: select, move the kept
+        rows to the front, and set context_lens to the new lengths.  seq_lens [S]
+        int32 counts the tokens each sequence has had in all (it must not share
+        storage with context_lens).  Capturable in a CUDA graph."""
+        pa_evict_select(self.source, self.new_lens, self.weights, self.positions, context_lens,
+                        self.recorded_lens, seq_lens, self.sink, self.recent)
+        pa_evict_compact(key_cache, value_cache, self.weights, self.positions, self.source,
+                         self.new_lens, block_tables, context_lens, self.recorded_lens, seq_lens)
+        context_lens.copy_(self.new_lens)
+        self.recorded_lens.copy_(self.new_lens)

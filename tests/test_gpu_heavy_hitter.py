@@ -1,0 +1,204 @@
+"""The calls as a program makes them: packed prompts are written and attended to,
+their weights taken, the caches held to a budget, and decode steps run over what is
+left, with an eviction every few steps.  Every step is checked against the
+sequences' whole histories: what each slot holds is named by its position, and
+the attention over those positions is recomputed in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import evict_reference as ref
+from paged_kv_cache_444_b200 import (EvictionState, WeightsWorkspace, pa_check_error,
+                                     pa_decode_weights, pa_reshape_and_cache, prompt_step)
+from weights_reference import HALF, attend, out_bound
+
+pytestmark = pytest.mark.gpu
+H, HK, D, G = 8, 2, 64, 4
+LENS, BUDGET, SINK, RECENT = (70, 130, 33, 48), 48, 2, 10
+STEPS, EVERY = 34, 8
+
+
+class Run:
+    def __init__(self, dev, dtype, graph):
+        self.dev, self.dtype, self.graph = dev, dtype, graph
+        self.g = torch.Generator(device=dev).manual_seed(11)
+        self.S, self.scale = len(LENS), D ** -0.5
+        need = [-(-(max(n, BUDGET) + EVERY) // 16) for n in LENS]
+        self.tables = torch.full((self.S, max(need)), -1, dtype=torch.int32)
+        perm = torch.randperm(sum(need), generator=torch.Generator().manual_seed(3)).to(torch.int32)
+        at = 0
+        for s, m in enumerate(need):
+            self.tables[s, :m] = perm[at:at + m]
+            at += m
+        self.tables = self.tables.to(dev)
+        self.kc = torch.full((sum(need), 16, HK, D), float("nan"), dtype=dtype, device=dev)
+        self.vc = self.kc.clone()
+        self.ctx = torch.tensor(LENS, dtype=torch.int32, device=dev)
+        self.length = self.ctx.clone()
+        self.state = EvictionState(self.S, HK, max(LENS) + EVERY, BUDGET, dev, SINK, RECENT)
+        # histories: K and V of every position, and the weight each has received
+        self.k = [None] * self.S
+        self.v = [None] * self.S
+        self.received = [None] * self.S
+
+    def normal(self, *shape):
+        return torch.randn(shape, generator=self.g, device=self.dev).to(self.dtype)
+
+    def slots(self, s, first, n):
+        at = torch.arange(first, first + n, device=self.dev)
+        return self.tables[s, at // 16].long() * 16 + at % 16
+
+    def prompt(self):
+        T = sum(LENS)
+        q, k, v = self.normal(T, H, D), self.normal(T, HK, D), self.normal(T, HK, D)
+        starts = torch.tensor(np.concatenate([[0], np.cumsum(LENS)]), dtype=torch.int32,
+                              device=self.dev)
+        slots = torch.cat([self.slots(s, 0, n) for s, n in enumerate(LENS)])
+        out = prompt_step(q, k, v, self.kc, self.vc, slots, starts, self.scale,
+                          weights=self.state.weights, window=max(LENS))
+        torch.cuda.synchronize()
+        for s, n in enumerate(LENS):
+            b = int(starts[s])
+            self.k[s], self.v[s] = k[b:b + n], v[b:b + n]
+            self.received[s] = torch.zeros((HK, n), dtype=torch.float64, device=self.dev)
+            for h in range(H):
+                p, o, _, rel, pv = attend(q[b:b + n, h], k[b:b + n, h // G], v[b:b + n, h // G],
+                                          self.scale, 0)
+                lim = out_bound(o, pv, rel, n, 8.0, self.dtype, HALF[self.dtype])
+                assert ((out[b:b + n, h].double() - o).abs() <= lim).all()
+                self.received[s][h // G] += p.sum(0)
+
+    def kept(self, s, kv):
+        """Positions of the cached tokens, in slot order."""
+        n = int(self.ctx[s])
+        return ref.slot_positions(self.state.positions[s, kv].cpu().numpy(),
+                                  int(self.state.recorded_lens[s]), int(self.length[s]), n)
+
+    def check_cache(self):
+        """Rows and weights of every slot are those of the position it names."""
+        for s in range(self.S):
+            n = int(self.ctx[s])
+            at = torch.arange(n, device=self.dev)
+            blk, row = self.tables[s, at // 16].long(), at % 16
+            for kv in range(HK):
+                pos = self.kept(s, kv)
+                assert len(set(pos.tolist())) == n and pos.min() >= 0
+                assert pos.max() < int(self.length[s])
+                assert set(range(min(SINK, n))) <= set(pos.tolist())
+                latest = range(max(0, int(self.length[s]) - RECENT), int(self.length[s]))
+                assert set(latest) <= set(pos.tolist())
+                idx = torch.as_tensor(pos, device=self.dev)
+                assert torch.equal(self.kc[blk, row, kv], self.k[s][idx, kv])
+                assert torch.equal(self.vc[blk, row, kv], self.v[s][idx, kv])
+                want = self.received[s][kv][idx]
+                got = self.state.weights[s, kv, :n].double()
+                # each addition is off by the bound of weights_reference, below 2^-10 of
+                # the term here, and by half a step of the sum
+                assert ((got - want).abs() <= 2.0 ** -10 * want).all()
+
+    def evict(self):
+        w, p = self.state.weights.cpu().numpy(), self.state.positions.cpu().numpy()
+        source, new = ref.select(w, p, self.state.recorded_lens.cpu().numpy(),
+                                 self.length.cpu().numpy(), self.ctx.cpu().numpy(), BUDGET, SINK,
+                                 RECENT)
+        self.state.evict(self.kc, self.vc, self.tables, self.ctx, self.length)
+        torch.cuda.synchronize()
+        assert np.array_equal(self.state.source.cpu().numpy(), source)
+        assert np.array_equal(self.ctx.cpu().numpy(), new)
+
+    def decode(self):
+        """Buffers of a decode step, captured once if `graph`."""
+        self.q, self.nk, self.nv = (torch.empty((self.S, h, D), dtype=self.dtype, device=self.dev)
+                                    for h in (H, HK, HK))
+        self.out = torch.empty_like(self.q)
+        self.slot = torch.empty(self.S, dtype=torch.int64, device=self.dev)
+        # (kept: the captured graph writes to it at every replay)
+        self.ws = WeightsWorkspace.for_call(self.q, self.kc, self.tables)
+
+        def step():
+            pa_reshape_and_cache(self.nk, self.nv, self.kc, self.vc, self.slot)
+            pa_decode_weights(self.out, self.state.weights, self.ws, self.q, self.kc, self.vc,
+                              self.tables, self.ctx, self.scale, 1)
+
+        if not self.graph:
+            return step
+        captured = torch.cuda.CUDAGraph()
+        self.slot.fill_(-1)
+        with torch.cuda.graph(captured):
+            step()
+        return captured.replay
+
+
+@pytest.mark.parametrize("dtype,graph", [(torch.bfloat16, False), (torch.float16, True)])
+def test_prompt_evict_decode(dtype, graph, cuda_device):
+    r = Run(cuda_device, dtype, graph)
+    r.prompt()
+    r.check_cache()
+    r.evict()
+    r.check_cache()
+    step = r.decode()
+    p_half = 2.0 ** -16 if dtype == torch.bfloat16 else 2.0 ** -11
+    for i in range(STEPS):
+        r.q.copy_(r.normal(r.S, H, D))
+        r.nk.copy_(r.normal(r.S, HK, D))
+        r.nv.copy_(r.normal(r.S, HK, D))
+        r.slot.copy_(torch.cat([r.slots(s, int(r.ctx[s]), 1) for s in range(r.S)]))
+        r.ctx += 1
+        r.length += 1
+        step()
+        torch.cuda.synchronize()
+        for s in range(r.S):
+            r.k[s] = torch.cat([r.k[s], r.nk[s:s + 1]])
+            r.v[s] = torch.cat([r.v[s], r.nv[s:s + 1]])
+            r.received[s] = torch.nn.functional.pad(r.received[s], (0, 1))
+            for kv in range(HK):
+                idx = torch.as_tensor(r.kept(s, kv), device=r.dev)
+                n = idx.numel()
+                p, o, _, rel, pv = attend(r.q[s, kv * G:(kv + 1) * G], r.k[s][idx, kv],
+                                          r.v[s][idx, kv], r.scale)
+                lim = out_bound(o, pv, rel, n, 8.0, dtype, p_half)
+                err = (r.out[s, kv * G:(kv + 1) * G].double() - o).abs()
+                assert (err <= lim).all(), (i, s, kv, float((err / lim).max()))
+                r.received[s][kv].index_add_(0, idx, p.sum(0))
+        r.check_cache()
+        if i % EVERY == EVERY - 1:
+            r.evict()
+            r.check_cache()
+    pa_check_error()
+    assert int(r.length[2]) - int(r.ctx[2]) > 0       # even the short prompt was evicted from
+
+
+def test_state_is_graph_capturable(cuda_device):
+    """select, compact and the two length copies as one captured graph, replayed
+    on contents that differ each time."""
+    S, W, B = 3, 60, 20
+    state = EvictionState(S, 1, W, B, cuda_device, 1, 3)
+    kc = torch.arange(S * 4 * 16, device=cuda_device).half().view(-1, 16, 1, 1).expand(
+        -1, -1, 1, 64).contiguous()
+    vc = kc.clone()
+    tables = torch.arange(S * 4, dtype=torch.int32, device=cuda_device).view(S, 4)
+    ctx = torch.tensor([60, 21, 20], dtype=torch.int32, device=cuda_device)
+    length = ctx.clone()
+    graph = torch.cuda.CUDAGraph()
+    before = kc.clone()
+    with torch.cuda.graph(graph):
+        state.evict(kc, vc, tables, ctx, length)
+    for seed in (1, 2):
+        kc.copy_(before)
+        vc.copy_(before)
+        ctx.copy_(torch.tensor([60, 21, 20], dtype=torch.int32))
+        state.recorded_lens.zero_()
+        w = np.random.default_rng(seed).random((S, 1, W), dtype=np.float32)
+        state.weights.copy_(torch.as_tensor(w))
+        graph.replay()
+        torch.cuda.synchronize()
+        source, new = ref.select(w, np.zeros((S, 1, W), np.int32), [0] * S, [60, 21, 20],
+                                 np.array([60, 21, 20]), B, 1, 3)
+        assert np.array_equal(state.source.cpu().numpy(), source)
+        assert ctx.tolist() == new.tolist() == state.recorded_lens.tolist()
+        for s in range(S):
+            n = int(new[s])
+            rows = kc[tables[s].long(), :, 0, 0].flatten().float().cpu().numpy()[:n]
+            assert np.array_equal(rows, s * 64 + source[s, 0, :n])
+            assert np.array_equal(state.positions[s, 0, :n].cpu().numpy(), source[s, 0, :n])
+    pa_check_error()
