@@ -91,12 +91,13 @@ def decode_step(query, key, value, key_cache, value_cache, slot_mapping, block_t
 
 def prompt_step(query, key, value, key_cache, value_cache, slot_mapping, seq_starts, scale: float,
                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                weights: torch.Tensor | None = None, window: int = 0, stream=None) -> torch.Tensor:
+                weights: torch.Tensor | None = None, window: int | None = None,
+                stream=None) -> torch.Tensor:
     """The first step of packed prompts in one attention layer: write their K/V
     rows into the cache (pa_reshape_and_cache; key_cache None: no write), attend
     (pa_prompt_attention) and, when weights [S, Hk, max_tokens] is given, set the
     attention weight each token receives from the last `window` tokens of its
-    prompt (pa_prompt_weights).  All tensors live on one CUDA device."""
+    prompt, all of them if None (pa_prompt_weights).  All tensors live on one CUDA device."""
     T, H, _ = query.shape
     if out is None:
         out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
@@ -106,7 +107,8 @@ def prompt_step(query, key, value, key_cache, value_cache, slot_mapping, seq_sta
         pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, stream)
     pa_prompt_attention(out, lse, query, key, value, seq_starts, scale, stream)
     if weights is not None:
-        pa_prompt_weights(weights, query, key, lse, seq_starts, scale, window, stream)
+        pa_prompt_weights(weights, query, key, lse, seq_starts, scale,
+                          max(T, 1) if window is None else window, stream)
     return out
 
 
@@ -120,6 +122,8 @@ class EvictionState:
 
     def __init__(self, num_seqs: int, num_kv_heads: int, max_tokens: int, budget: int,
                  device: torch.device | str, sink: int = 4, recent: int = 0):
+        if min(sink, recent) < 0 or sink + recent > budget:
+            raise ValueError("sink + recent must lie within the budget")
         rows = (num_seqs, num_kv_heads)
         i32 = dict(dtype=torch.int32, device=device)
         self.sink, self.recent = int(sink), int(recent)

@@ -1203,7 +1203,6 @@ constexpr int64_t kSelectMaxTokens = 1 << 19;   // the list of moved slots fits 
 constexpr int kSelectSmem = 227 * 1024;
 constexpr int64_t kSelectRun = 2048;            // slots that make another CTA worth its barriers
 constexpr int64_t kSelectPerSm = 2;             // resident CTAs (of 512 threads)
-constexpr int64_t kSelectListBytes = 64 * 1024;
 constexpr int64_t kCompactManyCtas = 2048;
 
 template <int kThreadsN, bool kReg>
@@ -1260,18 +1259,21 @@ extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const f
   a.sink = static_cast<int>(sink);
   a.recent = static_cast<int>(recent);
   // clusters of up to eight CTAs: while all of them are resident at once and a
-  // CTA still has kSelectRun slots, and as many as the list of moved slots needs
+  // CTA still has kSelectRun slots, and as many as a CTA's share of the flags and
+  // of the list of moved slots needs
   const int64_t rows = num_seqs * num_kv_heads;
   const int64_t most = budget < max_tokens / 2 ? budget : max_tokens / 2;
   const long long sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
-  int c = 1;
-  while (c < 8 && ((rows * c * 2 <= sms * kSelectPerSm && max_tokens > 2 * c * kSelectRun) ||
-                   most / c * 4 > kSelectListBytes))
-    c *= 2;
-  const int run = (static_cast<int>((max_tokens + c - 1) / c) + 31) & ~31;
-  int shift = 0;                                  // list entries of a CTA: a power of two
-  while ((static_cast<int64_t>(c) << shift) < most) ++shift;
+  int c = 1, run = 0, shift = 0;
+  for (;; c *= 2) {
+    run = (static_cast<int>((max_tokens + c - 1) / c) + 31) & ~31;
+    shift = 0;                                    // list entries of a CTA: a power of two
+    while ((static_cast<int64_t>(c) << shift) < most) ++shift;
+    if (c == 8) break;
+    if (rows * c * 2 <= sms * kSelectPerSm && max_tokens > 2 * c * kSelectRun) continue;
+    if (SelectSmem<512, false>::bytes(run, 1 << shift) <= kSelectSmem / kSelectPerSm) break;
+  }
   if (run <= 128 * 8)
     return launch_select<128, true>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 512 * 8)

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from paged_kv_cache_444_b200 import _lib, pa_evict_compact, pa_evict_select
+from paged_kv_cache_444_b200 import EvictionState, _lib, pa_evict_compact, pa_evict_select
 
 OK, NULL, SHAPE, DTYPE, ALIGN, UNSUP, CUDA, BOUNDS = range(8)
 FAKE = 0x10000
@@ -139,3 +139,10 @@ PW_BASE = dict({k: FAKE for k in ("weights", "q", "k", "lse", "starts")}, qs=102
 ])
 def test_prompt_weights_refusals(want, kw):
     assert _call("pa_prompt_weights", PW_ORDER, PW_BASE, **kw) == want
+
+
+def test_eviction_state_refuses_a_budget_that_cannot_hold():
+    EvictionState(1, 1, 32, 8, "cpu", sink=3, recent=5)
+    for bad in (dict(sink=4, recent=5), dict(sink=9), dict(sink=-1), dict(recent=-1)):
+        with pytest.raises(ValueError):
+            EvictionState(1, 1, 32, 8, "cpu", **bad)

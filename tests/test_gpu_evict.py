@@ -125,6 +125,31 @@ def test_select_where_keys_do_not_fit_shared_memory(cuda_device):
     assert np.array_equal(b.source[0, 0].cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("budget", [12000, 16384])
+def test_select_many_rows_of_a_wide_table(budget, cuda_device):
+    """More rows than clusters for each fit the device, and tables so wide that one CTA's
+    flags and list would not fit its shared memory."""
+    S, W, n = 160, 1 << 19, 30000
+    g = torch.Generator(device=cuda_device).manual_seed(96)
+    weights = torch.rand((S, 1, W), generator=g, device=cuda_device)
+    positions = torch.zeros((S, 1, W), dtype=torch.int32, device=cuda_device)
+    lens = torch.full((S,), n, dtype=torch.int32, device=cuda_device)
+    zeros, new = torch.zeros_like(lens), torch.empty_like(lens)
+    source = torch.full((S, 1, budget), -7, dtype=torch.int32, device=cuda_device)
+    pa_evict_select(source, new, weights, positions, lens, zeros, lens.clone(), 4, 100)
+    torch.cuda.synchronize()
+    pa_check_error()
+    assert (new == budget).all()
+    for s in (0, 77, 159):
+        w = weights[s, 0, :n].cpu().numpy().astype(np.float64)
+        w[:4] = w[n - 100:] = np.inf
+        kept = np.zeros(n, bool)
+        kept[np.argsort(-w, kind="stable")[:budget]] = True
+        want = np.arange(budget)
+        want[~kept[:budget]] = budget + np.flatnonzero(kept[budget:])
+        assert np.array_equal(source[s, 0].cpu().numpy(), want)
+
+
 def test_select_reports_a_bad_context_length(cuda_device):
     b = Batch(cuda_device, (50, 60, 20), 2, 16, 92)
     b.t["ctx"] = _i32([50, 61, 20], cuda_device)      # past max_tokens
