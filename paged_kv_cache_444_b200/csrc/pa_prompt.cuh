@@ -88,7 +88,9 @@ struct PromptSmem {
   static constexpr int kSched = kMark + 4;               // unit count and per-warp sums
   static constexpr int kSeqs = (kSched + 128 + 15) & ~15;      // int4 per ranked sequence
   static constexpr int kList = kSeqs + 16 * kPromptRankSeqs;   // unit of each rank
-  static constexpr int kBytes = kList + 4 * kPromptRankUnits;
+  // per softmax warp: 32 output rows x 32 columns on their way out
+  static constexpr int kStore = (kList + 4 * kPromptRankUnits + 15) & ~15;
+  static constexpr int kBytes = kStore + 8 * 2048;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -454,20 +456,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (i < 0) break;
         PromptItem it;
         prompt_item(a, order, seqs, list, i, span, it);
-        if (n_q > 0 && !(ok = __all_sync(0xffffffffu, wait_or_abort(sb + L::kBarQFree,
-                                                                    (n_q - 1) & 1, abort_flag))))
-          break;
-        if (lane == 0) {
-          const int tiles = it.lim[1] > 0 ? 2 : 1;
-          mbar_arrive_expect_tx(sb + L::kBarQ, tiles * L::kSlabs * q_rows * 128);
-          for (int t = 0; t < tiles; ++t) {
-#pragma unroll
-            for (int b = 0; b < L::kSlabs; ++b)
-              tma_load_4d(sb + L::kQ + t * L::kQTile + b * L::kSlab, &qmap, sb + L::kBarQ, 0, b,
-                          it.kvh * G, it.q0 + it.tile_a + t * a.tile_tokens);
-          }
-        }
-        ++n_q;
+        // the first K block goes ahead of Q, which has to wait for the last
+        // item's S products
         const int nkb = max(it.nkb[0], it.nkb[1]);
         for (int j = 0; j < nkb; ++j, ++issued) {
           const int st = issued % NST;
@@ -485,6 +475,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           __syncwarp();
           k_issued = issued + 1;
+          if (j == 0) {
+            if (n_q > 0 && !(ok = __all_sync(0xffffffffu, wait_or_abort(
+                                 sb + L::kBarQFree, (n_q - 1) & 1, abort_flag))))
+              break;
+            if (lane == 0) {
+              const int tiles = it.lim[1] > 0 ? 2 : 1;
+              mbar_arrive_expect_tx(sb + L::kBarQ, tiles * L::kSlabs * q_rows * 128);
+              for (int t = 0; t < tiles; ++t) {
+#pragma unroll
+                for (int b = 0; b < L::kSlabs; ++b)
+                  tma_load_4d(sb + L::kQ + t * L::kQTile + b * L::kSlab, &qmap, sb + L::kBarQ, 0,
+                              b, it.kvh * G, it.q0 + it.tile_a + t * a.tile_tokens);
+              }
+            }
+            __syncwarp();
+            ++n_q;
+          }
           if (issued >= NST && !(ok = __all_sync(0xffffffffu, wait_or_abort(
                                      sb + L::kBarVEmpty + 8 * st, par, abort_flag))))
             break;
@@ -565,7 +572,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (!wait(sb + L::kBarVOk + 8 * vs, vpar) ||
               !wait(sb + L::kBarP + 8 * t, (done[t] + j) & 1))
             return false;
-          if (leader) issue_pv(t, vs, j == 0, lim[t] - j * kPrefillKeys);
+          if (leader) {
+            issue_pv(t, vs, j == 0, lim[t] - j * kPrefillKeys);
+            if (j == nkb[t] - 1) umma_commit(sb + L::kBarOFull + 8 * t);
+          }
           __syncwarp();
           return true;
         };
@@ -597,11 +607,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
         if (!ok) break;
-        if (leader) {
-          umma_commit(sb + L::kBarOFull);
-          if (nkb[1] > 0) umma_commit(sb + L::kBarOFull + 8);
-        }
-        __syncwarp();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           done[t] += nkb[t];
@@ -700,14 +705,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const bool marked = *mark != 0;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN stays one
       const size_t hrow = static_cast<size_t>(it.q0 + tok) * a.num_heads + it.kvh * G + row % G;
-      uint16_t* o_row = a.out + hrow * D;
       if (live && a.lse) a.lse[hrow] = m * kLn2 + logf(l);
+      // 32 columns at a time through shared memory (16-byte chunk c of row r at
+      // c ^ (r / 2 % 4), free of bank conflicts), so that four lanes store a row's
+      // 64 bytes: a lane a row touched 32 lines a store, and the epilogue took
+      // 3700 to 6000 cycles an item
+      const uint32_t stage = sb + L::kStore + warp * 2048;
+      const int r0 = warp & 3;                         // this warp's rows: 32 r0 ..
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
         tmem_ld32(o_addr + 32 * c, o);
-        if (!live) continue;
-        if (marked) {
+        if (c == D / 32 - 1) {                         // O_t is in registers
+          tmem_fence_before_sync();
+          mbar_arrive(sb + L::kBarOFree + 8 * t);
+        }
+        if (marked && live) {
           // what the guard took out, for the keys this row sees
           for (int j = (it.tile_a + 1) / kPrefillKeys * kPrefillKeys; j < lim; ++j) {
             const uint16_t* v = a.value + (it.q0 + j) * a.value_stride + it.kvh * D + 32 * c;
@@ -718,18 +731,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
         }
+        __syncwarp();                                  // the rows before have been read
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          sts128(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4),
+                 pack2<BF16>(o[8 * q + 0] * inv, o[8 * q + 1] * inv),
+                 pack2<BF16>(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                 pack2<BF16>(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                 pack2<BF16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+        __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          const int r = 8 * q + (lane >> 2), ch = lane & 3, tr = 32 * r0 + r;
           uint4 v;
-          v.x = pack2<BF16>(o[8 * q + 0] * inv, o[8 * q + 1] * inv);
-          v.y = pack2<BF16>(o[8 * q + 2] * inv, o[8 * q + 3] * inv);
-          v.z = pack2<BF16>(o[8 * q + 4] * inv, o[8 * q + 5] * inv);
-          v.w = pack2<BF16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv);
-          *reinterpret_cast<uint4*>(o_row + 32 * c + 8 * q) = v;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(stage + r * 64 + ((ch ^ (r >> 1 & 3)) << 4)));
+          const int rt = it.tile_a + t * a.tile_tokens + tr / G;
+          if (tr < q_rows && rt < it.len)
+            *reinterpret_cast<uint4*>(a.out +
+                (static_cast<size_t>(it.q0 + rt) * a.num_heads + it.kvh * G + tr % G) * D +
+                32 * c + 8 * ch) = v;
         }
       }
-      tmem_fence_before_sync();
-      mbar_arrive(sb + L::kBarOFree + 8 * t);
       ++items;
     }
   }
