@@ -564,14 +564,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int nkb[2] = {warp_uniform(it.nkb[0]), warp_uniform(it.nkb[1])};
         const int lim[2] = {warp_uniform(it.lim[0]), warp_uniform(it.lim[1])};
         const int blocks = max(nkb[0], nkb[1]);
-        // P_t of block j (stage vs, phase vpar) is in: its product, after the
-        // epilogue has read the last item's O_t
-        auto pv = [&](int t, int j, int vs, int vpar) {
+        // P_t of block j (stage vs) is in: its product, after the epilogue has
+        // read the last item's O_t
+        auto pv = [&](int t, int j, int vs) {
           if (j == 0 && items[t] > 0 && !wait(sb + L::kBarOFree + 8 * t, (items[t] - 1) & 1))
             return false;
-          if (!wait(sb + L::kBarVOk + 8 * vs, vpar) ||
-              !wait(sb + L::kBarP + 8 * t, (done[t] + j) & 1))
-            return false;
+          if (!wait(sb + L::kBarP + 8 * t, (done[t] + j) & 1)) return false;
           if (leader) {
             issue_pv(t, vs, j == 0, lim[t] - j * kPrefillKeys);
             if (j == nkb[t] - 1) umma_commit(sb + L::kBarOFull + 8 * t);
@@ -581,14 +579,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         if (!(ok = wait(sb + L::kBarQ, n_q & 1))) break;
         ++n_q;
-        int last = 0, lpar = 0;            // the block before: stage and phase
+        if (!(ok = wait(sb + L::kBarKFull + 8 * st, par))) break;
+        int last = 0;                      // the stage of the block before
         for (int j = 0; j <= blocks && ok; ++j) {
-          if (j < blocks && !(ok = wait(sb + L::kBarKFull + 8 * st, par))) break;
           if (j < nkb[0]) {
             if (leader) issue_s(0, st);
             __syncwarp();
           }
-          if (j > 0 && j - 1 < nkb[1] && !(ok = pv(1, j - 1, last, lpar))) break;
+          if (j > 0 && j - 1 < nkb[1] && !(ok = pv(1, j - 1, last))) break;
           if (leader) {
             if (j > 0) umma_commit(sb + L::kBarVEmpty + 8 * last);
             if (j < nkb[1]) issue_s(1, st);
@@ -596,14 +594,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (j == blocks - 1) umma_commit(sb + L::kBarQFree);
           }
           __syncwarp();
-          if (j < nkb[0] && !(ok = pv(0, j, st, par))) break;
           if (j < blocks) {
+            // V of this block and K of the next one, while P_A is on its way
+            if (!(ok = wait(sb + L::kBarVOk + 8 * st, par))) break;
             last = st;
-            lpar = par;
             if (++st == NST) {
               st = 0;
               par ^= 1;
             }
+            if (j + 1 < blocks && !(ok = wait(sb + L::kBarKFull + 8 * st, par))) break;
+            if (j < nkb[0] && !(ok = pv(0, j, last))) break;
           }
         }
         if (!ok) break;
