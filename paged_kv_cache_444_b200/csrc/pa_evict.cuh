@@ -102,11 +102,9 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 ld_cluster_u32x4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void add_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v)
+               : "memory");
 }
 
 template <int kThreadsN, bool kReg>
@@ -217,63 +215,75 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
   auto mine = [&](int q) { return q < w1 && q * 32 + lane < run; };
 
   // The digit of T from the cluster's summed histogram: (bin, how many of its
-  // keys stay, how many there are).
+  // keys stay, how many there are).  The other CTAs add their bins that are not
+  // empty, few of the 2048, to the first one's, which finds the digit for all (a
+  // sum by every CTA over all bins took 5.5 k cycles with eight of them).
   uint32_t need = B;
   auto digit = [&](int pass) -> uint4 {
-    if (C > 1) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     constexpr int kQuads = kBins / kThreadsN / 4;      // uint4 of bins a thread
-    const uint32_t* hist = hist_of(pass);
+    uint32_t* hist = hist_of(pass);
     const int top = kBins - 4 * kQuads * (tid + 1);    // this thread's bins, from the top
-    uint4 c[kQuads];
-    uint32_t own = 0;
+    if (C > 1) {
+      if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (rank != 0) {
+        const uint32_t to = map_cluster(smem_addr(&hist[top]), 0);
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      c[q] = *reinterpret_cast<const uint4*>(&hist[top + 4 * q]);
-      if (C > 1) {
-        const uint32_t at = smem_addr(&hist[top + 4 * q]);
+        for (int q = 0; q < 4 * kQuads; ++q)
+          if (hist[top + q]) add_cluster_u32(to + 4 * q, hist[top + q]);
+      }
+      cluster_sync();
+    }
+    if (rank == 0) {
+      uint4 c[kQuads];
+      uint32_t own = 0;
 #pragma unroll
-        for (int r = 1; r < 8; ++r) {
-          if (r < C) {
-            const uint4 v = ld_cluster_u32x4(map_cluster(at, (rank + r) % C));
-            c[q].x += v.x;
-            c[q].y += v.y;
-            c[q].z += v.z;
-            c[q].w += v.w;
+      for (int q = 0; q < kQuads; ++q) {
+        c[q] = *reinterpret_cast<const uint4*>(&hist[top + 4 * q]);
+        own += (c[q].x + c[q].y) + (c[q].z + c[q].w);
+      }
+      uint32_t incl = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      uint32_t above = incl - own;
+#pragma unroll
+      for (int v = 0; v < kWarpsN; ++v)
+        if (v < warp) above += scan[v];
+      if (above < need && above + own >= need) {       // one thread
+        uint4 found = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = kQuads - 1; q >= 0; --q) {
+          const uint32_t bins[4] = {c[q].w, c[q].z, c[q].y, c[q].x};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (above < need && above + bins[e] >= need)
+              found = make_uint4(top + 4 * q + 3 - e, need - above, bins[e], 0);
+            above += bins[e];
           }
         }
-      }
-      own += (c[q].x + c[q].y) + (c[q].z + c[q].w);
-    }
-    uint32_t incl = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    uint32_t above = incl - own;
-#pragma unroll
-    for (int v = 0; v < kWarpsN; ++v)
-      if (v < warp) above += scan[v];
-    if (above < need && above + own >= need) {        // one thread
-#pragma unroll
-      for (int q = kQuads - 1; q >= 0; --q) {
-        const uint32_t bins[4] = {c[q].w, c[q].z, c[q].y, c[q].x};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (above < need && above + bins[e] >= need)
-            pick[pass] = make_uint4(top + 4 * q + 3 - e, need - above, bins[e], 0);
-          above += bins[e];
+        pick[pass] = found;
+        for (int r = 1; r < C; ++r) {
+          const uint32_t to = map_cluster(smem_addr(&pick[pass]), r);
+          st_cluster_u32(to, found.x);
+          st_cluster_u32(to + 4, found.y);
+          st_cluster_u32(to + 8, found.z);
         }
       }
     }
-    __syncthreads();
+    if (C > 1) cluster_sync();
+    else __syncthreads();
     return pick[pass];
   };
 
-  __syncthreads();                                     // the histograms are clear
+  // the histograms are clear; the cluster's are known to be before the first
+  // CTA's is added to
+  if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  __syncthreads();
   uint32_t* h0 = hist_of(0);
   each([&](int q, const uint32_t (&k)[kBatch], bool whole) {
 #pragma unroll
