@@ -1205,14 +1205,14 @@ constexpr int64_t kSelectRun = 2048;            // slots that make another CTA w
 constexpr int64_t kSelectPerSm = 2;             // resident CTAs (of 512 threads)
 constexpr int64_t kCompactManyCtas = 2048;
 
-template <int kThreadsN, bool kReg>
+template <int kThreadsN, int kHeld>
 pa_status launch_select(const EvictArgs& a, int64_t rows, int cluster, int run, int shift,
                         cudaStream_t stream) {
-  auto kernel = evict_select_kernel<kThreadsN, kReg>;
+  auto kernel = evict_select_kernel<kThreadsN, kHeld>;
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kernel, kSelectSmem, &done)) return PA_ERR_CUDA;
   return launch_ex(kernel, static_cast<unsigned>(rows * cluster), kThreadsN,
-                   SelectSmem<kThreadsN, kReg>::bytes(run, 1 << shift), stream, cluster, a, run, shift);
+                   SelectSmem<kThreadsN, kHeld>::bytes(run, 1 << shift), stream, cluster, a, run, shift);
 }
 
 // The arguments both calls share (host only, no CUDA calls).
@@ -1272,13 +1272,18 @@ extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const f
     while ((static_cast<int64_t>(c) << shift) < most) ++shift;
     if (c == 8) break;
     if (rows * c * 2 <= sms * kSelectPerSm && max_tokens > 2 * c * kSelectRun) continue;
-    if (SelectSmem<512, false>::bytes(run, 1 << shift) <= kSelectSmem / kSelectPerSm) break;
+    if (SelectSmem<512, 0>::bytes(run, 1 << shift) <= kSelectSmem / kSelectPerSm) break;
   }
-  if (run <= 128 * 8)
-    return launch_select<128, true>(a, rows, c, run, shift, as_stream(stream));
-  if (run <= 512 * 8)
-    return launch_select<512, true>(a, rows, c, run, shift, as_stream(stream));
-  return launch_select<512, false>(a, rows, c, run, shift, as_stream(stream));
+  // short runs: keys in registers, with room for a budget of 1024, 4096 or 8192
+  // and the tokens since the last eviction.  While all CTAs are resident, twice
+  // the threads for half the words each (8 x 8 rows of 2065 slots: 12.3 -> 10.3 us;
+  // with 128 x 8 rows of 4113 it would be 59 us against 31)
+  if (run <= 128 * 9) return launch_select<128, 9>(a, rows, c, run, shift, as_stream(stream));
+  if (run <= 512 * 9 && rows * c <= sms * kSelectPerSm)
+    return launch_select<512, 9>(a, rows, c, run, shift, as_stream(stream));
+  if (run <= 256 * 18) return launch_select<256, 18>(a, rows, c, run, shift, as_stream(stream));
+  if (run <= 512 * 18) return launch_select<512, 18>(a, rows, c, run, shift, as_stream(stream));
+  return launch_select<512, 0>(a, rows, c, run, shift, as_stream(stream));
 }
 
 extern "C" pa_status pa_evict_compact(void* key_cache, void* value_cache, float* weights,

@@ -44,16 +44,18 @@ __device__ __forceinline__ long long slot_position(const int32_t* positions, int
 // Select.  Every slot gets a 32-bit key that orders as its claim does: the
 // weight's bits made monotone (-0 as +0, NaN below every number), all ones for
 // a sink or a recent token.  The budget-th largest key T comes from a radix
-// select over 11, 11 and 10 bits; kept are the keys above T and, of those
-// equal to it, the lowest slots that fill the budget.
+// select; kept are the keys above T and, of those equal to it, the lowest slots
+// that fill the budget.
 //
 // One cluster of C CTAs takes a (sequence, KV head), each CTA a run of its
-// slots, each warp a share of the run in words of 32 slots.  The row is gone
-// through twice: once for the histogram of the top digit, and once, that digit
-// known, to flag the keys above it (a bit a slot) and to list those that share
-// it, few as a rule, from which the other two digits follow.  (A warp with more of
-// them than its list holds goes through its words again instead; up to 8 words a
-// warp stay in registers.)  The CTAs add up their histograms through
+// slots, each warp a share of the run in words of 32 slots.  A long run is gone
+// through twice: once for the histogram of the top digit (of 11, 11 and 10 bits),
+// and once, that digit known, to flag the keys above it (a bit a slot) and to list
+// those that share it, few as a rule, from which the other two digits follow.  (A
+// warp with more of them than its list holds goes through its words again
+// instead.)  A short run's keys stay in registers, for four digits of 8 bits,
+// whose histograms are quicker to clear and to scan.  The CTAs add up their
+// histograms through
 // distributed shared memory, and every one finds the same digit.  Then a thread
 // takes whole words: an exclusive scan of popcounts over threads and CTAs gives
 // every hole and every kept token behind the new length its rank.  The latter
@@ -61,27 +63,30 @@ __device__ __forceinline__ long long slot_position(const int32_t* positions, int
 // shared memory, where the holes fetch theirs.
 //
 // What bounds it is instructions and the barriers between the steps, not bytes
-// (4 a slot).  8 x 8 rows of 32768 to 131072 slots: 35 us; 105 us when every key
+// (4 a slot).  8 x 8 rows of 32768 to 131072 slots: 33 us; 105 us when every key
 // was built again for each digit and ranked a slot at a time (315 instructions
-// a word).  128 x 8 rows of 1017 slots: 14.7 us with 128 threads and the keys in
-// registers, 31 us with 512.  A CTA's steps on the long rows, in cycles: top
-// digit 7.2 k and its exchange 5.8 k, flags and lists 9.7 k, the other digits
-// 8 k, ranks and list 10 k.
+// a word).  128 x 8 rows of 1017 slots: 12.4 us, 31 us with 512 threads and three
+// digits of 11 bits.  One row of 131072 slots, eight CTAs: 22.5 us; in cycles, its
+// top digit 3.2 k and the exchange 3.8 k, flags and lists 6.3 k, the other digits
+// 9.3 k, ranks and list 9 k.
 // ---------------------------------------------------------------------------
-constexpr int kBins = 1 << 11;
 
-template <int kThreadsN, bool kReg>
+// kHeld: words of keys a warp keeps in registers, or 0: it loads them again
+template <int kThreadsN, int kHeld>
 struct SelectSmem {
   static constexpr int kWarpsN = kThreadsN / 32;
-  static constexpr int kListed = kReg ? 0 : 256;   // keys of T's first digit a warp lists
-  // [three histograms] [candidates: key, slot] [2 sums a warp] [totals] [pick]
+  static constexpr int kListed = kHeld ? 0 : 256;  // keys of T's first digit a warp lists
+  static constexpr int kDigit = kHeld ? 8 : 11;    // bits of a digit (the last: what is left)
+  static constexpr int kDigits = (32 + kDigit - 1) / kDigit;
+  static constexpr int kBins = 1 << kDigit;
+  // [a histogram a digit] [candidates: key, slot] [2 sums a warp] [totals] [pick]
   // [flag words] [equal words] [list of moved slots]
   static constexpr int kHist = 0;
-  static constexpr int kCand = kHist + 3 * kBins * 4;
+  static constexpr int kCand = kHist + kDigits * kBins * 4;
   static constexpr int kScan = kCand + kWarpsN * kListed * 8;
   static constexpr int kTotals = kScan + 2 * kWarpsN * 4;
   static constexpr int kPick = kTotals + 4 * 4;
-  static constexpr int kFlags = kPick + 3 * 16;
+  static constexpr int kFlags = kPick + kDigits * 16;
   // bytes for a run of `run` slots and `list` entries of the list
   static __host__ __device__ constexpr int bytes(int run, int list) {
     return kFlags + (run + 31) / 32 * 8 + 4 * list;
@@ -107,12 +112,14 @@ __device__ __forceinline__ void add_cluster_u32(uint32_t addr, uint32_t v) {
                : "memory");
 }
 
-template <int kThreadsN, bool kReg>
+template <int kThreadsN, int kHeld>
 __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
     evict_select_kernel(const EvictArgs a, int max_run, int list_shift) {
-  using L = SelectSmem<kThreadsN, kReg>;
-  constexpr int kWarpsN = L::kWarpsN;
-  constexpr int kBatch = 8;                            // words a warp loads before it uses any
+  using L = SelectSmem<kThreadsN, kHeld>;
+  constexpr bool kReg = kHeld > 0;
+  constexpr int kWarpsN = L::kWarpsN, kBins = L::kBins;
+  constexpr int kBatch = kReg ? 9 : 8;                 // words a warp loads before it uses any
+  static_assert(kHeld % 9 == 0, "words in registers come in whole batches");
   extern __shared__ __align__(16) uint8_t smem[];
   uint2* cand = reinterpret_cast<uint2*>(smem + L::kCand);
   uint32_t* scan = reinterpret_cast<uint32_t*>(smem + L::kScan);
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
   const int row = blockIdx.x / C;                      // s * Hk + kv
   const int s = row / a.num_kv_heads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int b = tid; b < 3 * kBins / 4; b += kThreadsN)
+  for (int b = tid; b < L::kDigits * kBins / 4; b += kThreadsN)
     reinterpret_cast<uint4*>(smem + L::kHist)[b] = make_uint4(0, 0, 0, 0);
   pdl_launch_dependents();
   pdl_wait();
@@ -193,18 +200,22 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
     }
     return false;
   };
-  uint32_t held_keys[kBatch];
-  if constexpr (kReg) load(w0, held_keys);
+  uint32_t held_keys[kReg ? kHeld : 1];
+  if constexpr (kReg) {
+#pragma unroll
+    for (int i = 0; i < kHeld; i += kBatch) {
+      uint32_t k[kBatch];
+      load(w0 + i, k);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) held_keys[i + u] = k[u];
+    }
+  }
   // f(first word, keys, whether every slot of the words is one of the run)
   auto each = [&](auto&& f) {
-    if constexpr (kReg) {
-      f(w0, held_keys, false);
-    } else {
-      for (int q = w0; q < w1; q += kBatch) {
-        uint32_t k[kBatch];
-        if (load(q, k)) f(q, k, true);
-        else f(q, k, false);
-      }
+    for (int q = w0; q < w1; q += kBatch) {
+      uint32_t k[kBatch];
+      if (load(q, k)) f(q, k, true);
+      else f(q, k, false);
     }
   };
   auto hist_of = [&](int pass) {
@@ -221,26 +232,26 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
   uint32_t need = B;
   auto digit = [&](int pass) -> uint4 {
     __syncthreads();
-    constexpr int kQuads = kBins / kThreadsN / 4;      // uint4 of bins a thread
+    constexpr int kPer = kBins > kThreadsN ? kBins / kThreadsN : 1;   // bins a thread
     uint32_t* hist = hist_of(pass);
-    const int top = kBins - 4 * kQuads * (tid + 1);    // this thread's bins, from the top
+    const int top = kBins - kPer * (tid + 1);          // this thread's bins, from the top
+    const bool any = top >= 0;
     if (C > 1) {
       if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-      if (rank != 0) {
+      if (rank != 0 && any) {
         const uint32_t to = map_cluster(smem_addr(&hist[top]), 0);
 #pragma unroll
-        for (int q = 0; q < 4 * kQuads; ++q)
+        for (int q = 0; q < kPer; ++q)
           if (hist[top + q]) add_cluster_u32(to + 4 * q, hist[top + q]);
       }
       cluster_sync();
     }
     if (rank == 0) {
-      uint4 c[kQuads];
-      uint32_t own = 0;
+      uint32_t c[kPer], own = 0;
 #pragma unroll
-      for (int q = 0; q < kQuads; ++q) {
-        c[q] = *reinterpret_cast<const uint4*>(&hist[top + 4 * q]);
-        own += (c[q].x + c[q].y) + (c[q].z + c[q].w);
+      for (int q = 0; q < kPer; ++q) {
+        c[q] = any ? hist[top + q] : 0u;
+        own += c[q];
       }
       uint32_t incl = own;
 #pragma unroll
@@ -257,14 +268,10 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
       if (above < need && above + own >= need) {       // one thread
         uint4 found = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int q = kQuads - 1; q >= 0; --q) {
-          const uint32_t bins[4] = {c[q].w, c[q].z, c[q].y, c[q].x};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (above < need && above + bins[e] >= need)
-              found = make_uint4(top + 4 * q + 3 - e, need - above, bins[e], 0);
-            above += bins[e];
-          }
+        for (int q = kPer - 1; q >= 0; --q) {
+          if (above < need && above + c[q] >= need)
+            found = make_uint4(top + q, need - above, c[q], 0);
+          above += c[q];
         }
         pick[pass] = found;
         for (int r = 1; r < C; ++r) {
@@ -284,26 +291,53 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
   // CTA's is added to
   if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   __syncthreads();
-  uint32_t* h0 = hist_of(0);
-  each([&](int q, const uint32_t (&k)[kBatch], bool whole) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (whole || mine(q + u)) atomicAdd(&h0[k[u] >> 21], 1u);
-  });
-  const uint4 d0 = digit(0);
-  need = d0.y;
-  uint32_t* h1 = hist_of(1);
-  uint2* wcand = cand + warp * L::kListed;             // this warp's list
-  int listed_keys = 0;
   const uint32_t below = (1u << lane) - 1;
-  each([&](int q, const uint32_t (&k)[kBatch], bool whole) {
-    uint32_t word = 0;                                 // lane u: the flags of word q + u
+  uint32_t T = 0;
+  bool cut = false;                                    // only some keys equal to T stay
+  if constexpr (kReg) {
+    uint4 d = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const uint32_t top = k[u] >> 21;
-      const uint32_t f = __ballot_sync(0xffffffffu, top > d0.x);
-      if (lane == u) word = f;
-      if constexpr (!kReg) {
+    for (int pass = 0; pass < L::kDigits; ++pass) {
+      const int shift = 32 - L::kDigit * (pass + 1);
+      uint32_t* h = hist_of(pass);
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (mine(w0 + u) && (pass == 0 || held_keys[u] >> (shift + L::kDigit) == T))
+          atomicAdd(&h[(held_keys[u] >> shift) & (kBins - 1)], 1u);
+      d = digit(pass);
+      need = d.y;
+      T = T << L::kDigit | d.x;
+    }
+    cut = d.z != need;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const bool in = mine(w0 + u);
+      const uint32_t f = __ballot_sync(0xffffffffu, in && (cut ? held_keys[u] > T : held_keys[u] >= T));
+      const uint32_t e = __ballot_sync(0xffffffffu, in && cut && held_keys[u] == T);
+      if (lane == 0 && w0 + u < w1) {
+        flags[w0 + u] = f;
+        same[w0 + u] = e;
+      }
+    }
+  } else {
+    uint32_t* h0 = hist_of(0);
+    each([&](int q, const uint32_t (&k)[kBatch], bool whole) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (whole || mine(q + u)) atomicAdd(&h0[k[u] >> 21], 1u);
+    });
+    const uint4 d0 = digit(0);
+    need = d0.y;
+    uint32_t* h1 = hist_of(1);
+    uint2* wcand = cand + warp * L::kListed;             // this warp's list
+    int listed_keys = 0;
+    each([&](int q, const uint32_t (&k)[kBatch], bool whole) {
+      uint32_t word = 0;                                 // lane u: the flags of word q + u
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t top = k[u] >> 21;
+        const uint32_t f = __ballot_sync(0xffffffffu, top > d0.x);
+        if (lane == u) word = f;
         const bool c = top == d0.x && (whole || mine(q + u));
         const uint32_t m = __ballot_sync(0xffffffffu, c);
         if (m) {
@@ -312,41 +346,41 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
           listed_keys += __popc(m);
         }
       }
-    }
-    if (lane < kBatch && (whole || q + lane < w1)) {
-      flags[q + lane] = word;
-      same[q + lane] = 0;
-    }
-  });
-  const bool listed = !kReg && listed_keys <= L::kListed;   // else this warp goes through its words again
-  __syncwarp();
-  // f(key, slot) over this warp's keys that share T's first digit
-  auto candidates = [&](auto&& f) {
-    if (listed) {
-      for (int i = lane; i < listed_keys; i += 32) f(wcand[i].x, static_cast<int>(wcand[i].y));
-    } else {
-      each([&](int q, const uint32_t (&k)[kBatch], bool) {
+      if (lane < kBatch && (whole || q + lane < w1)) {
+        flags[q + lane] = word;
+        same[q + lane] = 0;
+      }
+    });
+    const bool listed = listed_keys <= L::kListed;     // else this warp goes through its words again
+    __syncwarp();
+    // f(key, slot) over this warp's keys that share T's first digit
+    auto candidates = [&](auto&& f) {
+      if (listed) {
+        for (int i = lane; i < listed_keys; i += 32) f(wcand[i].x, static_cast<int>(wcand[i].y));
+      } else {
+        each([&](int q, const uint32_t (&k)[kBatch], bool) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if ((k[u] >> 21) == d0.x && mine(q + u)) f(k[u], (q + u) * 32 + lane);
-      });
-    }
-  };
-  candidates([&](uint32_t k, int) { atomicAdd(&h1[(k >> 10) & 2047u], 1u); });
-  const uint4 d1 = digit(1);
-  need = d1.y;
-  uint32_t* h2 = hist_of(2);
-  const uint32_t prefix = d0.x << 11 | d1.x;
-  candidates([&](uint32_t k, int) {
-    if ((k >> 10) == prefix) atomicAdd(&h2[k & 1023u], 1u);
-  });
-  const uint4 d2 = digit(2);
-  need = d2.y;
-  const uint32_t T = prefix << 10 | d2.x;
-  const bool cut = d2.z != need;                       // only some keys equal to T stay
-  candidates([&](uint32_t k, int i) {
-    if (k >= T) atomicOr(cut && k == T ? &same[i >> 5] : &flags[i >> 5], 1u << (i & 31));
-  });
+          for (int u = 0; u < kBatch; ++u)
+            if ((k[u] >> 21) == d0.x && mine(q + u)) f(k[u], (q + u) * 32 + lane);
+        });
+      }
+    };
+    candidates([&](uint32_t k, int) { atomicAdd(&h1[(k >> 10) & 2047u], 1u); });
+    const uint4 d1 = digit(1);
+    need = d1.y;
+    uint32_t* h2 = hist_of(2);
+    const uint32_t prefix = d0.x << 11 | d1.x;
+    candidates([&](uint32_t k, int) {
+      if ((k >> 10) == prefix) atomicAdd(&h2[k & 1023u], 1u);
+    });
+    const uint4 d2 = digit(2);
+    need = d2.y;
+    T = prefix << 10 | d2.x;
+    cut = d2.z != need;
+    candidates([&](uint32_t k, int i) {
+      if (k >= T) atomicOr(cut && k == T ? &same[i >> 5] : &flags[i >> 5], 1u << (i & 31));
+    });
+  }
   __syncthreads();
 
   // ---- ranks, a thread a share of whole words ----

@@ -107,9 +107,27 @@ def test_select_matches_the_plain_form(name, cuda_device):
     Batch(cuda_device, ctx, Hk, budget, 500 + len(name), **kw).check_select(sink, recent)
 
 
+@pytest.mark.parametrize("weights", [None, _ties, _odd], ids=["random", "ties", "odd"])
+@pytest.mark.parametrize("n,budget,recorded", [(1100, 1000, 1000), (4113, 4096, 4096),
+                                               (9000, 5000, 0), (12000, 3500, 3500)])
+def test_select_with_more_rows_than_ctas_at_once(n, budget, recorded, weights, cuda_device):
+    """300 rows: one CTA a row, its keys in registers up to 9216 slots."""
+    S = 300
+    b = Batch(cuda_device, (n,) * S, 1, budget, 97, weights=weights,
+              recorded=(recorded,) * S if recorded else None)
+    b.select(4, 60)
+    torch.cuda.synchronize()
+    pa_check_error()
+    got = b.source.cpu().numpy()
+    for s in (0, 101, 202, 299):
+        want = ref.select_row(b.weights[s, 0], b.positions[s, 0], recorded, int(b.length[s]), n,
+                              budget, 4, 60)
+        assert np.array_equal(got[s, 0], want), s
+
+
 def test_select_where_keys_do_not_fit_shared_memory(cuda_device):
     """The longest context the call takes: a CTA's run of 65536 slots is read
-    again for every digit.  numpy's stable sort stands in for the slow loop."""
+    again after its first digit.  numpy's stable sort stands in for the slow loop."""
     n, B, sink, recent = 524288, 200000, 4, 1000
     b = Batch(cuda_device, (n,), 1, B, 91)
     b.select(sink, recent)
