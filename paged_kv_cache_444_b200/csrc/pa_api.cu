@@ -1365,11 +1365,34 @@ WeightsLayout weights_layout(int64_t S, int64_t H, int64_t D, int64_t MB, int64_
   return l;
 }
 
+// One CTA a whole context (and no second launch) when a context is one partition
+// anyway, or when there are CTAs for two waves and contexts long enough for the
+// CTA's own last step to be small beside its pages.  128 x 8 contexts of 512 to
+// 4096 tokens: 207.6 us split, 198 single; 130 x 8 of 100 to 30000: 1338, 1297; but
+// 200 x 8 of up to 1000: 82, 90, and 112 x 8 of 4096 each (2.02 waves): 321, 333.
+#ifndef PA_WEIGHTS_SINGLE
+#define PA_WEIGHTS_SINGLE 6   // contexts an SM, at least (three CTAs are resident)
+#endif
+#ifndef PA_WEIGHTS_SINGLE_PARTS
+#define PA_WEIGHTS_SINGLE_PARTS 4   // partitions of the longest context, at least
+#endif
+
 template <int D, bool BF16, int NT>
 pa_status launch_weights_t(const CUtensorMap& km, const CUtensorMap& vm, const WeightsArgs& a,
                            long long items, long long merge, cudaStream_t stream) {
   constexpr int NST = Stages<D>::value;
   using L = DecodeSmem<D, NST>;
+  const long long rows = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
+  const long long sms = sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  if (a.parts == 1 ||
+      (rows >= PA_WEIGHTS_SINGLE * sms && a.parts >= PA_WEIGHTS_SINGLE_PARTS)) {
+    auto single = weights_single_kernel<D, NST, BF16, NT>;
+    static std::atomic<uint64_t> done_single{0};
+    if (!ensure_smem(single, L::kAlloc, &done_single)) return PA_ERR_CUDA;
+    return launch_ex(single, static_cast<unsigned>(rows), kThreads, L::kAlloc, stream, 1, km, vm,
+                     a);
+  }
   auto kernel = weights_split_kernel<D, NST, BF16, NT>;
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kernel, L::kAlloc, &done)) return PA_ERR_CUDA;

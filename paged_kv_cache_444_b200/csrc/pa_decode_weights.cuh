@@ -21,10 +21,12 @@
 // 193 us for 1.26 GB, 6.5 TB/s).  K and V are loaded evict-first, so that the
 // logits, small enough for L2 (16 bytes a token at G = 4), are still there when
 // the second pass reads them: it reads 4 MB of its 58 from DRAM, and costs the
-// call another 20 us, most of it latency at the first pass's end (with a CTA a
-// row of outputs and 1024 tokens a CTA the two took 234 us, now 214; with 512
-// threads, or 1024 or 2048 tokens, 216 to 221).  8 sequences of 32768 to 131072
-// tokens: 460 us, the second pass 35 of them.
+// call another 15 us, most of it latency at the first pass's end.  8 sequences of
+// 32768 to 131072 tokens: 460 us, the second pass 35 of them.
+//
+//   weights_single_kernel  both in one, a CTA per (sequence, KV head), where there
+//     are enough of those: the CTA knows its heads' lse at the end of its own
+//     pages.  The 128 sequences above: 198 us.
 #pragma once
 
 #include "pa_decode.cuh"
@@ -349,6 +351,198 @@ __global__ void __launch_bounds__(kThreads)
   });
 }
 
+// weights[t] += sum_g 2^(z_tg - lse_g) for tokens t0 <= t < t1 (set from `fresh`
+// on), by the kThreadsN threads of a CTA, kWeightsBatch tokens a thread at a time.
+template <int kThreadsN>
+__device__ __forceinline__ void add_weights(const float* z, float* w, int t0, int t1, int fresh,
+                                            int G, const float* lse_sh, int tid) {
+  constexpr int kStep = kThreadsN * kWeightsBatch;
+  for (int b0 = t0; b0 < t1; b0 += kStep) {
+    // whole batches of tokens that are not new need no checks, and take four
+    // heads a load
+    if ((G & 3) == 0 && b0 + kStep <= min(t1, fresh)) {
+      const float4* zt = reinterpret_cast<const float4*>(z + static_cast<size_t>(b0 + tid) * G);
+      float* wt = w + b0 + tid;
+      float sum[kWeightsBatch];
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) sum[u] = wt[u * kThreadsN];
+      for (int g = 0; g < G; g += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(lse_sh + g);
+        float4 v[kWeightsBatch];
+#pragma unroll
+        for (int u = 0; u < kWeightsBatch; ++u)
+          v[u] = zt[(u * kThreadsN * G + g) >> 2];
+#pragma unroll
+        for (int u = 0; u < kWeightsBatch; ++u)
+          sum[u] += (ex2(v[u].x - l.x) + ex2(v[u].y - l.y)) +
+                    (ex2(v[u].z - l.z) + ex2(v[u].w - l.w));
+      }
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) wt[u * kThreadsN] = sum[u];
+      continue;
+    }
+    float sum[kWeightsBatch] = {};
+    for (int g = 0; g < G; ++g) {
+      float v[kWeightsBatch];
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) {
+        const int t = b0 + u * kThreadsN + tid;
+        v[u] = t < t1 ? z[static_cast<size_t>(t) * G + g] : -INFINITY;
+      }
+#pragma unroll
+      for (int u = 0; u < kWeightsBatch; ++u) sum[u] += ex2(v[u] - lse_sh[g]);
+    }
+#pragma unroll
+    for (int u = 0; u < kWeightsBatch; ++u) {
+      const int t = b0 + u * kThreadsN + tid;
+      if (t < t1) w[t] = t < fresh ? w[t] + sum[u] : sum[u];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One CTA a (sequence, KV head), the whole context: the heads' lse is known at
+// the end of its own page loop, so the CTA turns its logits into weights itself
+// and writes the outputs, with no partials and no second launch.
+// Sequences are taken longest first (up to kLptMaxSeqs of them).
+// ---------------------------------------------------------------------------
+template <int D, int NST, bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads)
+    weights_single_kernel(const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap vmap, const WeightsArgs a) {
+  using L = DecodeSmem<D, NST>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(16) float lse_sh[16];
+  __shared__ int chosen;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  prefetch_tensormap(&kmap);
+  prefetch_tensormap(&vmap);
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int cap = a.max_blocks_per_seq * kPage;
+  const int kvh = blockIdx.x % a.num_kv_heads;
+  int s = blockIdx.x / a.num_kv_heads;
+  if (a.num_seqs > 1 && a.num_seqs <= kLptMaxSeqs) {
+    // the s-th longest sequence, ties by index: ranks counted on one 32-bit key
+    // each, (length << 8 | 255 - index), four at a time
+    unsigned* keys = reinterpret_cast<unsigned*>(smem);   // stage area, not in use yet
+    const int n4 = (a.num_seqs + 3) / 4;
+    for (int i = tid; i < 4 * n4; i += kThreads) {
+      const int c = i < a.num_seqs ? min(max(a.context_lens[i], 0), (1 << 24) - 1) : 0;
+      keys[i] = i < a.num_seqs ? static_cast<unsigned>(c) << 8 | (255 - i) : 0u;
+    }
+    __syncthreads();
+    for (int i = tid; i < a.num_seqs; i += kThreads) {
+      const unsigned key = keys[i];
+      int rank = 0;
+      for (int j = 0; j < n4; ++j) {
+        const uint4 v = reinterpret_cast<const uint4*>(keys)[j];
+        rank += (v.x > key) + (v.y > key) + (v.z > key) + (v.w > key);
+      }
+      if (rank == s) chosen = i;
+    }
+    __syncthreads();
+    s = chosen;
+    fence_proxy_async_smem();   // before TMA writes to the stage area
+    __syncthreads();
+  }
+  int ctx = a.context_lens[s];
+  if (ctx < 0 || ctx > cap) {
+    if (tid == 0 && kvh == 0) record_error(kErrContextLen, s);
+    ctx = ctx < 0 ? 0 : cap;
+  }
+  const int group = a.group;
+  const size_t hrow0 = static_cast<size_t>(s) * a.num_heads + static_cast<size_t>(kvh) * group;
+  if (ctx == 0) {
+    for (int i = tid; i < group * D; i += kThreads) a.out[hrow0 * D + i] = 0;
+    return;
+  }
+  const int n_pages = (ctx + kPage - 1) / kPage;
+  const int my_pages = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;
+  const uint32_t stage0 = smem_addr(smem) + warp * NST * L::kStageBytes;
+  const uint32_t bar0 = smem_addr(smem + L::kBarOffset) + warp * NST * 8;
+  init_ring<NST>(bar0, lane);
+
+  // block ids 32 at a time, one a lane, the next 32 on their way
+  const size_t row_base = static_cast<size_t>(s) * a.max_blocks_per_seq;
+  auto load_ids = [&](int win) -> int {
+    const int k = win * 32 + lane;
+    if (k >= my_pages) return -1;
+    const size_t at = row_base + warp + static_cast<size_t>(k) * kWarps;
+    const int id = a.block_tables[at];
+    if (id >= 0 && id < a.num_blocks) return id;
+    record_error(kErrBlockId, static_cast<long long>(at));
+    return -1;   // a box at a negative row reads zeros
+  };
+  int win = 0, ids = load_ids(0), ids_next = my_pages > 32 ? load_ids(1) : -1;
+  const uint64_t once = evict_first_policy();
+  auto issue = [&](int k) {   // whole warp; lane 0 loads this warp's page k
+    const int row = __shfl_sync(0xffffffffu, (k >> 5) == win ? ids : ids_next, k & 31) * kPage;
+    if (lane == 0) {
+      const uint32_t bar = bar0 + (k % NST) * 8;
+      const uint32_t dk = stage0 + (k % NST) * L::kStageBytes, dv = dk + L::kPageBytes;
+      mbar_arrive_expect_tx(bar, L::kStageBytes);
+#pragma unroll
+      for (int b = 0; b < L::kBoxesPerRow; ++b)
+        tma_load_4d_once(dk + b * kBoxBytes, &kmap, bar, 0, b, kvh, row, once);
+#pragma unroll
+      for (int b = 0; b < L::kBoxesPerRow; ++b)
+        tma_load_4d_once(dv + b * kBoxBytes, &vmap, bar, 0, b, kvh, row, once);
+    }
+  };
+  for (int k = 0; k < min(my_pages, NST); ++k) issue(k);
+
+  WeightsWarp<D, BF16, NT> st;
+  st.init(a.query + hrow0 * D, group, lane);
+  float* z = a.logits + (static_cast<size_t>(s) * a.num_kv_heads + kvh) * cap * group;
+  bool ok = true;
+  int k_stop = my_pages;
+  for (int k = 0; k < my_pages; ++k) {
+    if (k > 0 && (k & 31) == 0) {
+      ++win;
+      ids = ids_next;
+      ids_next = my_pages > (win + 1) * 32 ? load_ids(win + 1) : -1;
+    }
+    if (!__all_sync(~0u, mbar_wait_bounded(bar0 + (k % NST) * 8, (k / NST) & 1))) {
+      if (lane == 0) record_error(kErrWaitTimeout, blockIdx.x);
+      ok = false;
+      k_stop = k;
+      break;
+    }
+    const uint32_t kb = stage0 + (k % NST) * L::kStageBytes;
+    const int tok0 = (warp + k * kWarps) * kPage;
+    if (tok0 + kPage > ctx) zero_page_tail<L::kBoxesPerRow>(kb + L::kPageBytes, ctx - tok0, lane);
+    st.page(kb, kb + L::kPageBytes, ctx - tok0, a.scale_log2, lane,
+            z + static_cast<size_t>(tok0) * group, group);
+    __syncwarp();
+    if (k + NST < my_pages) issue(k + NST);
+  }
+  // (a warp that gave up first waits for the loads it still has in flight; then
+  // the CTA ends without a result)
+  if (!__syncthreads_and(drain_stages<NST>(ok, k_stop, my_pages, bar0) && ok)) return;
+  st.publish(reinterpret_cast<float*>(smem) + warp * group * D,
+             reinterpret_cast<float*>(smem + L::kRedMOffset) + warp * 16,
+             reinterpret_cast<float*>(smem + L::kRedLOffset) + warp * 16, group, lane);
+  __syncthreads();
+  merge_and_emit<D, NST>(smem, group, false, 1, 0,
+                         [&](int g, int d, float o0, float o1, float big_m, float big_l) {
+    const float inv = big_l > 0.f ? 1.f / big_l : (big_l == 0.f ? 0.f : big_l);
+    *reinterpret_cast<uint32_t*>(a.out + (hrow0 + g) * D + d) = pack2<BF16>(o0 * inv, o1 * inv);
+    if (d == 0) lse_sh[g] = big_l == 0.f ? INFINITY : big_m + __log2f(big_l);
+  });
+  __syncthreads();   // the lse, and every warp's logits
+  if (ctx > a.max_tokens) {
+    if (tid == 0 && kvh == 0) record_error(kErrContextLen, s);
+    return;
+  }
+  add_weights<kThreads>(z, a.weights + (static_cast<size_t>(s) * a.num_kv_heads + kvh) *
+                                           a.max_tokens,
+                        0, ctx, max(ctx - a.new_tokens, 0), group, lse_sh, tid);
+}
+
 // lse (log2 units) of one head from its partitions, whole warp; +inf when no
 // token has a finite logit, so that every weight comes out 0.
 __device__ __forceinline__ float warp_lse(const float* m, const float* l, int np, int lane) {
@@ -396,48 +590,7 @@ __global__ void __launch_bounds__(kWeightsThreads)
     const float* z = a.logits + static_cast<size_t>(row) * cap * G;
     float* w = a.weights + static_cast<size_t>(row) * a.max_tokens;
     const int fresh = max(ctx - a.new_tokens, 0);      // tokens from here on start anew
-    constexpr int kStep = kWeightsThreads * kWeightsBatch;
-    for (int b0 = t0; b0 < t1; b0 += kStep) {
-      // whole batches of tokens that are not new need no checks, and take four
-      // heads a load
-      if ((G & 3) == 0 && b0 + kStep <= min(t1, fresh)) {
-        const float4* zt = reinterpret_cast<const float4*>(z + static_cast<size_t>(b0 + tid) * G);
-        float* wt = w + b0 + tid;
-        float sum[kWeightsBatch];
-#pragma unroll
-        for (int u = 0; u < kWeightsBatch; ++u) sum[u] = wt[u * kWeightsThreads];
-        for (int g = 0; g < G; g += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(lse_sh + g);
-          float4 v[kWeightsBatch];
-#pragma unroll
-          for (int u = 0; u < kWeightsBatch; ++u)
-            v[u] = zt[(u * kWeightsThreads * G + g) >> 2];
-#pragma unroll
-          for (int u = 0; u < kWeightsBatch; ++u)
-            sum[u] += (ex2(v[u].x - l.x) + ex2(v[u].y - l.y)) +
-                      (ex2(v[u].z - l.z) + ex2(v[u].w - l.w));
-        }
-#pragma unroll
-        for (int u = 0; u < kWeightsBatch; ++u) wt[u * kWeightsThreads] = sum[u];
-        continue;
-      }
-      float sum[kWeightsBatch] = {};
-      for (int g = 0; g < G; ++g) {
-        float v[kWeightsBatch];
-#pragma unroll
-        for (int u = 0; u < kWeightsBatch; ++u) {
-          const int t = b0 + u * kWeightsThreads + tid;
-          v[u] = t < t1 ? z[static_cast<size_t>(t) * G + g] : -INFINITY;
-        }
-#pragma unroll
-        for (int u = 0; u < kWeightsBatch; ++u) sum[u] += ex2(v[u] - lse_sh[g]);
-      }
-#pragma unroll
-      for (int u = 0; u < kWeightsBatch; ++u) {
-        const int t = b0 + u * kWeightsThreads + tid;
-        if (t < t1) w[t] = t < fresh ? w[t] + sum[u] : sum[u];
-      }
-    }
+    add_weights<kWeightsThreads>(z, w, t0, t1, fresh, G, lse_sh, tid);
   }
 
   // ---- this run's share of the heads' outputs, a row a warp or several ----

@@ -1,6 +1,7 @@
 """pa_decode_weights against attention and its weights in 64 bits."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -88,6 +89,24 @@ def test_matches_the_definition(name, cuda_device):
     torch.cuda.synchronize()
     pa_check_error()
     _check(b, before, weights, out, new, b.cfg.scale)
+
+
+@pytest.mark.parametrize("S,H,Hk,D,dtype", [(120, 16, 8, 128, "bf16"), (120, 128, 8, 64, "f16"),
+                                            (300, 4, 4, 128, "f16"), (230, 20, 4, 64, "bf16")])
+def test_batches_that_take_a_cta_a_context(S, H, Hk, D, dtype, cuda_device):
+    """Enough contexts for two waves of CTAs, ranked by length (up to 256 sequences)
+    or not: mostly short ones, empty ones and some of several id windows."""
+    rng = np.random.default_rng(S)
+    ctx = rng.integers(0, 60, S)
+    ctx[[3, S // 2, S - 1]] = (2200, 1777, 2049)
+    b = _batch(cuda_device, [int(c) for c in ctx], H, Hk, D, dtype, 960 + S)
+    poison_past_context(b)
+    weights = torch.rand((S, Hk, 2300), device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights)
+    torch.cuda.synchronize()
+    pa_check_error()
+    _check(b, before, weights, out, 1, b.cfg.scale)
 
 
 @pytest.mark.parametrize("dtype,heads", [("bf16", 8), ("f16", 8), ("bf16", 20)])
