@@ -1615,8 +1615,50 @@ pa_status launch_prompt_weights_t(const CUtensorMap& qm, const CUtensorMap& km,
   if (!ensure_smem(kernel, L::kAlloc, &done)) return PA_ERR_CUDA;
   const long long sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
-  return launch_ex(kernel, static_cast<unsigned>(items < sms ? items : sms), kPwThreads, L::kAlloc,
-                   stream, 1, qm, km, a);
+  // A cluster an item while the items would not fill the SMs one and a half times
+  // and every CTA of it has a query tile; and, with many tiles (long items, whose
+  // lengths differ), while they would not fill them four times.  Eight CTAs only
+  // for very few items: clusters that large leave SMs out.  4096 tokens, 32/8 heads:
+  // 176 us without, 108 with four, 133 with eight; 1000 tokens: 49 and 25; but 900 +
+  // 77 + 400 tokens of 32 heads, 256 items: 20 and, with two, 25.
+  const int tiles = (a.window + a.tile_tokens - 1) / a.tile_tokens;
+  PromptWeightsArgs args = a;
+  args.cluster = 1;
+  for (int next = 2; next <= (items * 4 < sms ? 8 : 4); next *= 2) {
+    const long long ctas = items * args.cluster;
+    if (!(2 * ctas < 3 * sms && next <= tiles) && !(ctas < 4 * sms && 16 * next <= tiles)) break;
+    args.cluster = next;
+  }
+  // as many clusters as are resident at once: one more would take a second wave
+  long long room = sms;
+  if (args.cluster > 1) {
+    static std::atomic<int> cache[kMaxDevices][4] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
+    std::atomic<int>& known = cache[dev][args.cluster / 4 + 1];   // 2, 4, 8 -> 1, 2, 3
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(args.cluster, 1, 1);
+      cfg.blockDim = dim3(kPwThreads, 1, 1);
+      cfg.dynamicSmemBytes = L::kAlloc;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = args.cluster;
+      attr.val.clusterDim.y = 1;
+      attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return PA_ERR_CUDA;
+      }
+      known.store(n, std::memory_order_relaxed);
+    }
+    room = n;
+  }
+  return launch_ex(kernel, static_cast<unsigned>((items < room ? items : room) * args.cluster),
+                   kPwThreads, L::kAlloc, stream, args.cluster, qm, km, args);
 }
 }  // namespace
 

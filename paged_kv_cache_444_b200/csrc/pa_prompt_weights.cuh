@@ -17,7 +17,9 @@
 // b of the even tiles and of the odd ones, each with an S^T buffer of its own, so
 // that the next tile's product runs during this one's 2^x and the four warps of a
 // scheduler are at different places.  At the end of an item the two partial sums
-// of a key meet in shared memory.  Warps: 0-15 the sums, 16 issues the MMAs, 17
+// of a key meet in shared memory.  Where there are few items, a cluster of up to
+// eight CTAs takes one: CTA r the query tiles r, r + C, ..., and the first CTA adds
+// the others' sums up, in their order, as they arrive in its shared memory.  Warps: 0-15 the sums, 16 issues the MMAs, 17
 // the loads, 18 brings each tile's lse into shared memory (negated, in log2 units).
 #pragma once
 
@@ -41,6 +43,7 @@ struct PromptWeightsArgs {
   int num_kv_heads;
   int group;
   int tile_tokens;
+  int cluster;                 // CTAs of an item
   int max_tokens;
   int window;
 };
@@ -65,14 +68,17 @@ struct PwSmem {
   static constexpr int kBarLFull = kBarQEmpty + 8 * NQ;
   static constexpr int kBarLEmpty = kBarLFull + 8 * NL;
   static constexpr int kBarSums = kBarLEmpty + 8 * NL;     // an item's partial sums are in
-  static constexpr int kBarEnd = kBarSums + 8;
+  static constexpr int kBarCFull = kBarSums + 8;           // the other CTAs' sums, two items,
+  static constexpr int kBarCFree = kBarCFull + 16;         // and that they have been added up
+  static constexpr int kBarEnd = kBarCFree + 16;
   static constexpr int kTmemSlot = kBarEnd + 8;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kSched = kAbort + 4;
   static constexpr int kSeqs = (kSched + 128 + 15) & ~15;
   static constexpr int kList = kSeqs + 16 * kPromptRankSeqs;
   static constexpr int kSums = kList + 4 * kPromptRankUnits;   // of two items: one float a key
-  static constexpr int kBytes = kSums + 2 * kPwSpan * 4;
+  static constexpr int kOthers = kSums + 2 * kPwSpan * 4;   // two items, 7 CTAs, a float a key
+  static constexpr int kBytes = kOthers + 2 * 7 * kPwSpan * 4;
   static constexpr int kAlloc = kBytes + 1024;        // one CTA per SM: both sizes pass 114 KB
   static_assert(kBytes > 114 * 1024, "one CTA holds all of an SM's tensor memory");
 };
@@ -80,14 +86,16 @@ struct PwSmem {
 struct PwItem {
   int s, kvh, q0, len;   // sequence, KV head, its first row and its length
   int k0;                // first key
-  int t0, tiles;         // first query token and the number of query tiles
   int blocks;            // key blocks
+  int t0, step, tiles;   // first token of this CTA's first query tile, tokens from one of its
+                         // tiles to the next, and their number
 };
 
 // The pairs of a sequence are ranked as the attention's are (more keys, more
 // work); here the first keys are seen by most tokens.
 __device__ __forceinline__ void pw_item(const PromptWeightsArgs& a, const PromptOrder& o,
-                                        const int4* seqs, const int* list, int i, PwItem& it) {
+                                        const int4* seqs, const int* list, int i, int rank,
+                                        PwItem& it) {
   const int u = i / a.num_kv_heads;
   it.kvh = i - u * a.num_kv_heads;
   const PromptUnit unit = prompt_unit(a, o, seqs, list, u, kPwSpan);
@@ -95,14 +103,41 @@ __device__ __forceinline__ void pw_item(const PromptWeightsArgs& a, const Prompt
   it.q0 = unit.q0;
   it.len = unit.len;
   it.k0 = ((it.len + kPwSpan - 1) / kPwSpan - 1 - unit.pair) * kPwSpan;
-  it.t0 = max(it.k0, it.len - a.window);
-  it.tiles = (it.len - it.t0 + a.tile_tokens - 1) / a.tile_tokens;
+  it.t0 = max(it.k0, it.len - a.window) + rank * a.tile_tokens;
+  it.step = a.cluster * a.tile_tokens;
+  it.tiles = max(0, it.len - it.t0 + it.step - 1) / it.step;
   it.blocks = min(kPwBlocks, (it.len - it.k0 + 127) / 128);
 }
 
-// The first query tile that sees a key of block b.
+// The first of its query tiles that sees a key of block b.
 __device__ __forceinline__ int pw_first(const PwItem& it, int tile_tokens, int b) {
-  return max(0, it.k0 + 128 * b - it.t0) / tile_tokens;
+  const int before = it.k0 + 128 * b - it.t0 - (tile_tokens - 1);   // its last token reaches the key
+  return before > 0 ? (before + it.step - 1) / it.step : 0;
+}
+
+// Barriers of another CTA of the cluster, and waits for what other CTAs wrote.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort_flag) {
+  const unsigned long long t0 = global_timer_ns();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    if (done) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      record_error(kErrWaitTimeout, blockIdx.x);
+      return false;
+    }
+  }
 }
 
 // sum += 2^(s scale + neg) over 32 columns, three pairs of eight on the FMA
@@ -149,7 +184,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
   const PromptOrder order = prompt_order(a, kPwSpan, reinterpret_cast<int*>(smem + L::kSched),
                                          seqs, list, warp, lane);
   const int total = order.total * a.num_kv_heads;
-  if (prefill_item_index(0, total, blockIdx.x, gridDim.x) < 0) return;
+  const int C = a.cluster, rank = blockIdx.x % C;
+  const int cid = blockIdx.x / C, clusters = gridDim.x / C;
+  if (prefill_item_index(0, total, cid, clusters) < 0) return;
   const int q_rows = a.tile_tokens * G;
   float* lse_sh = reinterpret_cast<float*>(smem + L::kLse);
 
@@ -164,6 +201,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       mbar_init(sb + L::kBarSEmpty + 8 * i, 128);
     }
     mbar_init(sb + L::kBarSums, 512);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sb + L::kBarCFull + 8 * i, max(1, C - 1) * kPwSpan);
+      mbar_init(sb + L::kBarCFree + 8 * i, kPwSpan);
+    }
     for (int i = 0; i < L::NQ; ++i) {
       mbar_init(sb + L::kBarQFull + 8 * i, 1);
       mbar_init(sb + L::kBarQEmpty + 8 * i, 1);
@@ -186,7 +227,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     fence_proxy_async_smem();
   }
   tmem_fence_before_sync();
-  __syncthreads();
+  if (C > 1) {
+    __syncwarp();
+    cluster_sync();            // every CTA's barriers are ready
+  } else {
+    __syncthreads();
+  }
   tmem_fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlot);
   auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -198,10 +244,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     int nk = 0, nq = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      const int i = prefill_item_index(k, total, cid, clusters);
       if (i < 0) break;
       PwItem it;
-      pw_item(a, order, seqs, list, i, it);
+      pw_item(a, order, seqs, list, i, rank, it);
+      if (it.tiles == 0) continue;
       const int ks = nk % L::NK;
       if (nk >= L::NK && !(ok = wait(sb + L::kBarKEmpty + 8 * ks, ((nk / L::NK) & 1) ^ 1))) break;
       if (lane == 0) {
@@ -224,7 +271,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           for (int c = 0; c < L::kSlabs; ++c)
             tma_load_4d(sb + L::kQ + qs * L::kTile + c * L::kSlab, &qmap,
                         sb + L::kBarQFull + 8 * qs, 0, c, it.kvh * G,
-                        it.q0 + it.t0 + j * a.tile_tokens);
+                        it.q0 + it.t0 + j * it.step);
         }
         __syncwarp();
         ++nq;
@@ -245,11 +292,12 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     int nk = 0, nq = 0, ns = 0;          // ns: bit 2 b + h the phase of that S buffer
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      const int i = prefill_item_index(k, total, cid, clusters);
       if (i < 0) break;
       PwItem it;
-      pw_item(a, order, seqs, list, i, it);
+      pw_item(a, order, seqs, list, i, rank, it);
       const int tiles = warp_uniform(it.tiles);
+      if (tiles == 0) continue;
       const int first1 = warp_uniform(it.blocks > 1 ? pw_first(it, a.tile_tokens, 1) : it.tiles);
       const int ks = nk % L::NK;
       if (!(ok = wait(sb + L::kBarKFull + 8 * ks, (nk / L::NK) & 1))) break;
@@ -294,13 +342,13 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     int n = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      const int i = prefill_item_index(k, total, cid, clusters);
       if (i < 0) break;
       PwItem it;
-      pw_item(a, order, seqs, list, i, it);
+      pw_item(a, order, seqs, list, i, rank, it);
       for (int j = 0; j < it.tiles; ++j, ++n) {
         const int sl = n % L::NL;
-        const int tok0 = it.t0 + j * a.tile_tokens;
+        const int tok0 = it.t0 + j * it.step;
         const int rows = min(a.tile_tokens, it.len - tok0) * G;
         float v[4];
 #pragma unroll
@@ -329,10 +377,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     int n = 0, ns = 0, items = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
+      const int i = prefill_item_index(k, total, cid, clusters);
       if (i < 0) break;
       PwItem it;
-      pw_item(a, order, seqs, list, i, it);
+      pw_item(a, order, seqs, list, i, rank, it);
       const int kb = it.k0 + 128 * b, kj = kb + key;
       const int first = b < it.blocks ? pw_first(it, a.tile_tokens, b) : it.tiles;
       float acc = 0.f;
@@ -342,7 +390,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         if (j >= first) {
           if (!(ok = wait(full, ns & 1))) break;
           tmem_fence_after_sync();
-          const int tok0 = it.t0 + j * a.tile_tokens;
+          const int tok0 = it.t0 + j * it.step;
           const int rows = min(a.tile_tokens, it.len - tok0) * G;
           const float4* lse4 = reinterpret_cast<const float4*>(lse_sh + sl * 128);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -396,17 +444,46 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       if (!(ok = wait(sb + L::kBarSums, items & 1))) break;
       ++items;
       if (h == 1) continue;
+      float sum = acc + part[128 * b + key];
+      if (C > 1) {
+        // slot: of two items; use: how often it has been used before
+        const int slot = (items - 1) & 1, use = (items - 1) >> 1;
+        const uint32_t cfull = sb + L::kBarCFull + 8 * slot, cfree = sb + L::kBarCFree + 8 * slot;
+        const uint32_t others = sb + L::kOthers + slot * 7 * kPwSpan * 4 + (128 * b + key) * 4;
+        if (rank > 0) {
+          if (use > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_cluster(cfree, (use - 1) & 1,
+                                                                          abort_flag)) != 0))
+            break;
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                           map_cluster(others + (rank - 1) * kPwSpan * 4, 0)), "f"(sum)
+                       : "memory");
+          mbar_arrive_cluster(map_cluster(cfull, 0));
+          continue;
+        }
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(cfull, use & 1, abort_flag)) != 0))
+          break;
+        for (int r = 0; r < C - 1; ++r) {
+          float v;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(others + r * kPwSpan * 4) : "memory");
+          sum += v;
+        }
+        for (int r = 1; r < C; ++r) mbar_arrive_cluster(map_cluster(cfree, r));
+      }
       if (it.len > a.max_tokens) {
         if (key == 0 && b == 0 && it.k0 == 0 && it.kvh == 0) record_error(kErrContextLen, it.s);
       } else if (kj < it.len && b < it.blocks) {
-        a.weights[(static_cast<size_t>(it.s) * a.num_kv_heads + it.kvh) * a.max_tokens + kj] =
-            acc + part[128 * b + key];
+        a.weights[(static_cast<size_t>(it.s) * a.num_kv_heads + it.kvh) * a.max_tokens + kj] = sum;
       }
     }
   }
 
   tmem_fence_before_sync();
-  __syncthreads();
+  if (C > 1) {
+    __syncwarp();
+    cluster_sync();            // no CTA leaves while another writes to it
+  } else {
+    __syncthreads();
+  }
   if (warp == kPwWarpMma) {
     tmem_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);

@@ -72,6 +72,12 @@ CASES = {
     "whole_gqa8_d64": ((1500, 1100), 8, 1, 64, "f16", 5000, {}),
     "whole_mha": ((1900, 1025), 2, 2, 128, "bf16", 1900, {}),
     "long_whole": ((6000,), 4, 1, 128, "bf16", 6000, {}),
+    # few items: clusters of 2, 4 and 8 CTAs, some without a tile of a key block
+    "pair_of_ctas": ((200,), 2, 1, 64, "f16", 130, {}),
+    "four_ctas": ((777, 5, 300), 4, 1, 128, "bf16", 140, dict(trail=7)),
+    "eight_ctas_mqa": ((3000, 1700), 16, 1, 128, "f16", 3000, dict(fused=True)),
+    "eight_ctas_group3": ((1000,), 6, 2, 64, "bf16", 1000, {}),
+    "eight_ctas_many_items": ((9000,), 16, 1, 64, "f16", 9000, {}),
 }
 
 
