@@ -28,6 +28,14 @@
 // the sequence's end) can carry one over, so warps 10-11 look through those
 // blocks of V, set what is not finite to 0 there and mark the CTA; from then on
 // its epilogues add such values to the rows that do see them.
+//
+// Measured (head_dim 128, bf16, 32 heads over 8): one prompt of 16384 tokens 1.71
+// to 1.77 ms, 1242 to 1284 TFLOP/s of the 1648 that cuBLAS reaches in short runs
+// (2.0 ms when repeated under the power cap, 1100 of 1374); eight prompts of
+// 77 to 4001 tokens 281 us, 1033 TFLOP/s.  Neither the tensor pipe (51 %) nor the
+// special-function unit (47 %) is full: a tile's chain S -> softmax -> P V takes
+// longer than the four products of both tiles, and two tiles in turn cover it in part.
+// Three tiles do not fit the 512 columns.  Figures of single choices are at them.
 #pragma once
 
 #include <limits.h>

@@ -19,8 +19,16 @@
 // scheduler are at different places.  At the end of an item the two partial sums
 // of a key meet in shared memory.  Where there are few items, a cluster of up to
 // eight CTAs takes one: CTA r the query tiles r, r + C, ..., and the first CTA adds
-// the others' sums up, in their order, as they arrive in its shared memory.  Warps: 0-15 the sums, 16 issues the MMAs, 17
-// the loads, 18 brings each tile's lse into shared memory (negated, in log2 units).
+// the others' sums up, in their order, as they arrive in its shared memory.  Warps: 0-15 the
+// sums, 16 issues the MMAs, 17 the loads, 18 brings each tile's lse into shared
+// memory (negated, in log2 units).
+//
+// Measured: prompts of 4096 and 1333 tokens, 32 heads of 128, whole: 115 us, 1.7
+// times what the 2^x alone take on the special-function unit; issue slots 55 % used,
+// special-function unit 47 %, tensor pipe 35 %.  Instead of the even/odd split, four
+// key blocks an item with a warpgroup each take 124 us, one block's columns over four
+// warpgroups 130.  One prompt of 4096 tokens, 32 heads over 8 (128 items): 109 us with
+// clusters, 176 without; of 1000 tokens 25 and 49.
 #pragma once
 
 #include "pa_prompt.cuh"
