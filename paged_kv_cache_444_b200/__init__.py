@@ -138,6 +138,8 @@ class EvictionState:
         rows to the front, and set context_lens to the new lengths.  seq_lens [S]
         int32 counts the tokens each sequence has had in all (it must not share
         storage with context_lens).  Capturable in a CUDA graph."""
+        if seq_lens.data_ptr() == context_lens.data_ptr() and context_lens.numel():
+            raise ValueError("seq_lens must not share storage with context_lens")
         pa_evict_select(self.source, self.new_lens, self.weights, self.positions, context_lens,
                         self.recorded_lens, seq_lens, self.sink, self.recent)
         pa_evict_compact(key_cache, value_cache, self.weights, self.positions, self.source,

@@ -403,7 +403,7 @@ def _prompt_rows(name, rows, T, D):
     shape, stride = rows.shape, rows.stride()
     if len(shape) != 3 or shape[0] != T or shape[2] != D:
         raise ValueError(f"{name} must be [num_tokens, heads, head_dim]")
-    if (stride[1] != D or stride[2] != 1) and rows.numel():
+    if (stride[1] != D and shape[1] > 1 or stride[2] != 1) and rows.numel():
         raise ValueError(f"{name} token rows must be dense")
     return stride[0] if T > 1 else shape[1] * D
 

@@ -146,3 +146,12 @@ def test_eviction_state_refuses_a_budget_that_cannot_hold():
     for bad in (dict(sink=4, recent=5), dict(sink=9), dict(sink=-1), dict(recent=-1)):
         with pytest.raises(ValueError):
             EvictionState(1, 1, 32, 8, "cpu", **bad)
+
+
+def test_eviction_state_refuses_lengths_in_one_tensor():
+    """The new lengths would overwrite the tokens a sequence has had."""
+    state = EvictionState(2, 1, 32, 8, "cpu")
+    kc = torch.zeros(4, 16, 1, 64, dtype=torch.float16)
+    lens = torch.full((2,), 20, dtype=torch.int32)
+    with pytest.raises(ValueError, match="seq_lens must not share"):
+        state.evict(kc, kc.clone(), torch.zeros(2, 2, dtype=torch.int32), lens, lens)

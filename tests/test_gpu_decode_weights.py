@@ -230,3 +230,49 @@ def test_workspace_too_small_is_refused(cuda_device):
     with pytest.raises(PagedAttentionError, match="PA_ERR_SHAPE"):
         _call(b, weights, new_tokens=-1)
     assert math.isfinite(float(weights.sum()))
+
+
+@pytest.mark.parametrize("n", [40, 1500], ids=["one_cta", "split"])
+def test_logits_that_are_all_minus_infinity(n, cuda_device):
+    """A product beyond 32 bits: out 0 and nothing added, as for an empty context."""
+    b = _batch(cuda_device, (n, 30), 4, 2, 64, "bf16", 938)
+    b.query[0] = 0
+    b.query[0, :, 0] = 3e38
+    own = b.block_tables[0, :-(-n // 16)].long()
+    b.key_cache[own] = 0
+    b.key_cache[own, :, :, 0] = -3e38
+    weights = torch.full((2, 2, n), 0.25, device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights, new_tokens=0)
+    torch.cuda.synchronize()
+    pa_check_error()
+    assert (out[0] == 0).all() and torch.equal(weights[0], before[0])
+    b.context_lens[0] = 0             # check the other sequence alone
+    _check(b, before, weights, out, 0, b.cfg.scale)
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    """Logits of 50 x 64 heads over tables of 700000 tokens, 2.2e9 in all, and as many weights."""
+    ctx = (5,) * 48 + (700_000, 600_001)
+    b = _batch(cuda_device, ctx, 64, 4, 64, "bf16", 939)
+    weights = torch.full((50, 4, 11_000_000), 0.5, device=cuda_device)
+    before = weights[:, :, :700_100].clone()
+    out = _call(b, weights)
+    torch.cuda.synchronize()
+    pa_check_error()
+    assert (weights[:, :, 700_100:] == 0.5).all()
+    _check(b, before, weights[:, :, :700_100], out, 1, b.cfg.scale)
+
+
+def test_offsets_beyond_32_bits_with_a_cta_a_context(cuda_device):
+    """Logits of 1100 x 64 heads over tables of 32768 tokens, 2.3e9 in all."""
+    ctx = (3, 40) * 549 + (32_768, 30_001)
+    b = _batch(cuda_device, ctx, 64, 4, 64, "f16", 940)
+    weights = torch.zeros((1100, 4, 32_768), device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights)
+    torch.cuda.synchronize()
+    pa_check_error()
+    b.context_lens[2:1096] = 0        # check the first and the last ones
+    out[2:1096], weights[2:1096] = 0, 0
+    _check(b, before, weights, out, 1, b.cfg.scale)

@@ -315,3 +315,42 @@ def test_select_on_another_stream_and_in_a_graph(cuda_device):
         torch.cuda.synchronize()
         assert np.array_equal(b.source.cpu().numpy(), b.want(2, 8)[0])
     pa_check_error()
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    """Weights of 520 x 8 rows of 2^19 columns and caches of 2.6e9 elements."""
+    S, Hk, W, B, D = 520, 8, 1 << 19, 40, 64
+    dev, g = cuda_device, torch.Generator(device=cuda_device).manual_seed(98)
+    weights = torch.full((S, Hk, W), 7.0, device=dev)
+    weights[:, :, :100] = torch.rand((S, Hk, 100), generator=g, device=dev)
+    positions = torch.full((S, Hk, W), -5, dtype=torch.int32, device=dev)
+    ctx = torch.full((S,), 97, dtype=torch.int32, device=dev)
+    rec, length = torch.zeros_like(ctx), ctx.clone()
+    source = torch.full((S, Hk, B), -7, dtype=torch.int32, device=dev)
+    new = torch.empty_like(ctx)
+    NB = 320_000
+    kc = torch.zeros((NB, 16, Hk, D), dtype=torch.float16, device=dev)
+    vc = torch.zeros_like(kc)
+    tables = torch.arange(S * 7, dtype=torch.int32, device=dev).view(S, 7)
+    tables = NB - 1 - tables.flip(0)                  # the last blocks belong to the last rows
+    at = tables.long()
+    kc[at], vc[at] = (torch.randn((S, 7, 16, Hk, D), generator=g, device=dev).half()
+                      for _ in range(2))
+    few = [0, 300, S - 2, S - 1]
+    w0 = weights[few, :, :97].cpu().numpy()
+    k0, v0 = (x[at[few]].cpu().view(torch.int16).numpy().reshape(-1, 16, Hk, D) for x in (kc, vc))
+    pa_evict_select(source, new, weights, positions, ctx, rec, length, 2, 5)
+    pa_evict_compact(kc, vc, weights, positions, source, new, tables, ctx, rec, length)
+    torch.cuda.synchronize()
+    pa_check_error()
+    p0, lens = np.zeros_like(w0, dtype=np.int32), np.full(4, 97, np.int32)
+    want, nw = ref.select(w0, p0, 0 * lens, lens, lens, B, 2, 5)
+    assert np.array_equal(source[few].cpu().numpy(), want) and (new == B).all()
+    local = np.arange(28, dtype=np.int32).reshape(4, 7)
+    k1, v1, w1, p1 = ref.compact(k0, v0, w0, p0, want, nw, local, lens, 0 * lens, lens)
+    for got, ours in ((kc, k1), (vc, v1)):
+        got = got[at[few]].cpu().view(torch.int16).numpy().reshape(-1, 16, Hk, D)
+        assert np.array_equal(got, ours)
+    assert np.array_equal(weights[few, :, :97].cpu().numpy(), w1)
+    assert np.array_equal(positions[few, :, :B].cpu().numpy(), p1[:, :, :B])
+    assert (positions[:, :, B:] == -5).all() and (weights[:, :, 100:] == 7).all()

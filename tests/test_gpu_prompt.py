@@ -236,3 +236,48 @@ def test_binding_refuses(cuda_device):
             pa_prompt_attention(**{**a, **bad})
     with pytest.raises(PagedAttentionError, match="PA_ERR_SHAPE"):
         pa_prompt_attention(**{**a, "scale": float("nan")})
+
+
+def test_rows_whose_logits_are_all_minus_infinity(cuda_device):
+    """A product beyond 32 bits: out 0 and lse -inf where a row sees nothing else, and no
+    weight on such keys where it does."""
+    p = Prompt(cuda_device, (300, 40), 4, 2, 64, "bf16", 88)
+    p.q[:, :, 0] = 3e38
+    p.k[:, :, 0] = 0
+    p.k[:260] = 0
+    p.k[:260, :, 0] = -3e38
+    p.run()
+    torch.cuda.synchronize()
+    pa_check_error()
+    assert (p.out[:260] == 0).all() and (p.lse[:260] == -torch.inf).all()
+    p.check(seqs=[1])
+    # the rows after them see keys 260.. alone
+    tail = Prompt(cuda_device, (40,), 4, 2, 64, "bf16", 88)
+    for name in "qkv":
+        getattr(tail, name).copy_(getattr(p, name)[260:300])
+    tail.scale = p.scale
+    tail.out, tail.lse = p.out[260:300], p.lse[260:300]
+    tail.check()
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    """140000 rows of 128 heads of 128 out of a fused projection: 2.3e9 elements of out."""
+    p = Prompt(cuda_device, (1,), 128, 8, 128, "bf16", 89)
+    lens, T = (1000,) * 140, 140000
+    x = torch.empty((T, 144, 128), dtype=torch.bfloat16, device=cuda_device)
+    x.normal_(generator=torch.Generator(device=cuda_device).manual_seed(90))
+    p.lens, p.T, p.q, p.k, p.v = lens, T, x[:, :128], x[:, 128:136], x[:, 136:]
+    p.starts = torch.arange(0, T + 1, 1000, dtype=torch.int32, device=cuda_device)
+    p.out = torch.full((T, 128, 128), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    p.lse = torch.full((T, 128), 7.0, device=cuda_device)
+    p.run().check(seqs=[0, 131, 139], heads=[0, 77, 127])
+
+
+def test_a_single_kv_head_may_have_any_head_stride(cuda_device):
+    p = Prompt(cuda_device, (70, 30), 4, 1, 64, "f16", 91)
+    want = p.run().out.clone()
+    wide = torch.zeros((100, 3, 64), dtype=torch.float16, device=cuda_device)
+    wide[:, 1] = p.k[:, 0]
+    p.k = wide.as_strided((100, 1, 64), (192, 8, 1), 64)      # one head: its stride says nothing
+    p.run().check()
+    assert torch.equal(p.out, want)

@@ -196,3 +196,10 @@ def test_binding_refuses(cuda_device):
         with pytest.raises(PagedAttentionError, match="PA_ERR_SHAPE"):
             pa_prompt_weights(**{**a, **bad})
     assert np.isfinite(float(a["weights"].sum()))
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    """Weights of 40 x 8 rows of 7 million columns, 2.2e9 in all."""
+    p = Prompt(cuda_device, tuple(range(1, 41)), 8, 8, 64, "f16", 79)
+    weights, lse = _run(p, 100, extra=7_000_000 - 40)
+    _check(p, weights, lse, 100, seqs=[0, 38, 39])
