@@ -78,12 +78,12 @@ struct SelectSmem {
   static constexpr int kDigit = kHeld ? 8 : 11;    // bits of a digit (the last: what is left)
   static constexpr int kDigits = (32 + kDigit - 1) / kDigit;
   static constexpr int kBins = 1 << kDigit;
-  // [a histogram a digit] [candidates: key, slot] [2 sums a warp] [totals] [pick]
+  // [a histogram a digit] [candidates: key, slot] [4 sums a warp] [totals] [pick]
   // [flag words] [equal words] [list of moved slots]
   static constexpr int kHist = 0;
   static constexpr int kCand = kHist + kDigits * kBins * 4;
   static constexpr int kScan = kCand + kWarpsN * kListed * 8;
-  static constexpr int kTotals = kScan + 2 * kWarpsN * 4;
+  static constexpr int kTotals = kScan + 4 * kWarpsN * 4;
   static constexpr int kPick = kTotals + 4 * 4;
   static constexpr int kFlags = kPick + kDigits * 16;
   // bytes for a run of `run` slots and `list` entries of the list
@@ -228,9 +228,40 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
   // keys stay, how many there are).  The other CTAs add their bins that are not
   // empty, few of the 2048, to the first one's, which finds the digit for all (a
   // sum by every CTA over all bins took 5.5 k cycles with eight of them).
+  // A CTA alone with few bins: every warp finds the digit for itself.
   uint32_t need = B;
   auto digit = [&](int pass) -> uint4 {
     __syncthreads();
+    if constexpr (kBins == 256) {
+      if (C == 1) {
+        const uint4* bins = reinterpret_cast<const uint4*>(hist_of(pass)) + 62 - 2 * lane;
+        const uint4 hi = bins[1], lo4 = bins[0];         // this lane's bins, from the top
+        const uint32_t c[8] = {hi.w, hi.z, hi.y, hi.x, lo4.w, lo4.z, lo4.y, lo4.x};
+        uint32_t own = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) own += c[q];
+        uint32_t incl = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        // the first lane whose bins reach `need`, and the bin of them that does
+        const int at = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+        uint32_t above = incl - own, x = 0, y = 0, z = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (above < need && above + c[q] >= need) {
+            x = 255 - 8 * lane - q;
+            y = need - above;
+            z = c[q];
+          }
+          above += c[q];
+        }
+        return make_uint4(__shfl_sync(0xffffffffu, x, at), __shfl_sync(0xffffffffu, y, at),
+                          __shfl_sync(0xffffffffu, z, at), 0);
+      }
+    }
     constexpr int kPer = kBins > kThreadsN ? kBins / kThreadsN : 1;   // bins a thread
     uint32_t* hist = hist_of(pass);
     const int top = kBins - kPer * (tid + 1);          // this thread's bins, from the top
@@ -295,8 +326,10 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
   bool cut = false;                                    // only some keys equal to T stay
   if constexpr (kReg) {
     uint4 d = make_uint4(0, 0, 0, 0);
+    int rest = 32;                                       // bits below T's digits so far
 #pragma unroll
     for (int pass = 0; pass < L::kDigits; ++pass) {
+      if (pass > 0 && d.z == need) break;                // all keys with these digits stay
       const int shift = 32 - L::kDigit * (pass + 1);
       uint32_t* h = hist_of(pass);
 #pragma unroll
@@ -306,7 +339,9 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
       d = digit(pass);
       need = d.y;
       T = T << L::kDigit | d.x;
+      rest = shift;
     }
+    T <<= rest;
     cut = d.z != need;
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
@@ -369,13 +404,16 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
     need = d1.y;
     uint32_t* h2 = hist_of(2);
     const uint32_t prefix = d0.x << 11 | d1.x;
-    candidates([&](uint32_t k, int) {
-      if ((k >> 10) == prefix) atomicAdd(&h2[k & 1023u], 1u);
-    });
-    const uint4 d2 = digit(2);
-    need = d2.y;
-    T = prefix << 10 | d2.x;
-    cut = d2.z != need;
+    T = prefix << 10;
+    if (d1.z != need) {                                  // else all keys with these digits stay
+      candidates([&](uint32_t k, int) {
+        if ((k >> 10) == prefix) atomicAdd(&h2[k & 1023u], 1u);
+      });
+      const uint4 d2 = digit(2);
+      need = d2.y;
+      T |= d2.x;
+      cut = d2.z != need;
+    }
     candidates([&](uint32_t k, int i) {
       if (k >= T) atomicOr(cut && k == T ? &same[i >> 5] : &flags[i >> 5], 1u << (i & 31));
     });
@@ -386,6 +424,7 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
   // exclusive scan of a pair of counts over the cluster's threads, in order of
   // the slots; every CTA calls it (it holds cluster barriers)
   auto before = [&](uint32_t x, uint32_t y, int slot) -> uint2 {
+    uint32_t* sums = scan + slot * 2 * kWarpsN;
     uint32_t ix = x, iy = y;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -396,8 +435,8 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
       }
     }
     if (lane == 31) {
-      scan[warp] = ix;
-      scan[kWarpsN + warp] = iy;
+      sums[warp] = ix;
+      sums[kWarpsN + warp] = iy;
     }
     __syncthreads();
     ix -= x;
@@ -409,8 +448,8 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
         ix += tx;
         iy += ty;
       }
-      tx += scan[v];
-      ty += scan[kWarpsN + v];
+      tx += sums[v];
+      ty += sums[kWarpsN + v];
     }
     if (C > 1) {
       if (tid == 0) {
@@ -422,8 +461,6 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
         ix += ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot]), c));
         iy += ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot + 1]), c));
       }
-    } else {
-      __syncthreads();                                 // the sums are used again
     }
     return make_uint2(ix, iy);
   };
@@ -465,8 +502,6 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
       else list[r] = slot;
     }
   }
-  if (C > 1) cluster_sync();
-  else __syncthreads();
   // a word's holes take consecutive entries: the word's first rank goes where
   // the word's equal bits were, and a warp then writes whole words
   r = first.x;
@@ -474,7 +509,8 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
     same[q] = r;
     r += __popc(front_bits(q) & ~flags[q]);
   }
-  __syncthreads();
+  if (C > 1) cluster_sync();
+  else __syncthreads();
   for (int q = warp; q * 32 < front; q += kWarpsN) {
     const uint32_t h = front_bits(q) & ~flags[q];
     int from = lo + q * 32 + lane;
