@@ -1277,7 +1277,14 @@ extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const f
   // short runs: keys in registers, with room for a budget of 1024, 4096 or 8192
   // and the tokens since the last eviction.  While all CTAs are resident, twice
   // the threads for half the words each (8 x 8 rows of 2065 slots: 12.3 -> 10.3 us;
-  // with 128 x 8 rows of 4113 it would be 59 us against 31)
+  // 128 x 8 rows of 4113 took 59 us against 31; as the kernel is now, 6.5 and 19.4)
+  // of many rows each takes a single warp, if that holds its keys (106 x 32 rows of
+  // 349 slots: 20.5 -> 13.7 us, 400 of 276: 8.1 -> 5.6; but two warps with 18
+  // words for 128 x 8 rows of 1017: 14.9 against 12.1)
+  if (run <= 32 * 9 && rows > sms)
+    return launch_select<32, 9>(a, rows, c, run, shift, as_stream(stream));
+  if (run <= 32 * 18 && rows > sms)
+    return launch_select<32, 18>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 128 * 9) return launch_select<128, 9>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 512 * 9 && rows * c <= sms * kSelectPerSm)
     return launch_select<512, 9>(a, rows, c, run, shift, as_stream(stream));

@@ -62,12 +62,13 @@ __device__ __forceinline__ long long slot_position(const int32_t* positions, int
 // shared memory, where the holes fetch theirs.
 //
 // What bounds it is instructions and the barriers between the steps, not bytes
-// (4 a slot).  8 x 8 rows of 32768 to 131072 slots: 33 us; 105 us when every key
+// (4 a slot).  8 x 8 rows of 32768 to 131072 slots: 32 us; 105 us when every key
 // was built again for each digit and ranked a slot at a time (315 instructions
-// a word).  128 x 8 rows of 1017 slots: 12.4 us, 31 us with 512 threads and three
-// digits of 11 bits.  One row of 131072 slots, eight CTAs: 22.5 us; in cycles, its
-// top digit 3.2 k and the exchange 3.8 k, flags and lists 6.3 k, the other digits
-// 9.3 k, ranks and list 9 k.
+// a word).  128 x 8 rows of 1017 slots: 9.2 us; 31 us with 512 threads and three
+// digits of 11 bits, 12.1 us with each word's bounds looked at in every pass.  One
+// row of 131072 slots, eight CTAs: 21.4 us, in cycles about a tenth each for the
+// top digit and its exchange, a fifth for flags and lists, the rest shared between
+// the other digits and the ranks and list.
 // ---------------------------------------------------------------------------
 
 // kHeld: words of keys a warp keeps in registers, or 0: it loads them again
@@ -199,14 +200,30 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
     }
     return false;
   };
+  // A short run's keys.  Those past its end, or in another warp's words, are 0.
+  // None but NaN's keys are that low, so they can only make T's last bin look
+  // fuller when T is 0; it then is cut, and the run's own slots come first.
   uint32_t held_keys[kReg ? kHeld : 1];
   if constexpr (kReg) {
+    const int i0 = w0 * 32 + lane;
+    const int mine = min(run, w1 * 32) - i0, noted = min(recorded, w1 * 32) - i0;
+    const int at = static_cast<int>(late) + i0;
+    // held: positions outside [sink, first_recent)
+    const uint32_t open = first_recent > a.sink ? first_recent - a.sink : 0;
 #pragma unroll
     for (int i = 0; i < kHeld; i += kBatch) {
-      uint32_t k[kBatch];
-      load(w0 + i, k);
+      float x[kBatch];
+      int p[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) held_keys[i + u] = k[u];
+      for (int u = 0; u < kBatch; ++u) {
+        x[u] = 32 * (i + u) < mine ? __ldg(w + i0 + 32 * (i + u)) : 0.f;
+        p[u] = 32 * (i + u) < noted ? __ldg(pos + i0 + 32 * (i + u)) : at + 32 * (i + u);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t k = static_cast<uint32_t>(p[u]) - a.sink >= open ? 0xffffffffu : claim_key(x[u]);
+        held_keys[i + u] = 32 * (i + u) < mine ? k : 0u;
+      }
     }
   }
   // f(first word, keys, whether every slot of the words is one of the run)
@@ -334,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
       uint32_t* h = hist_of(pass);
 #pragma unroll
       for (int u = 0; u < kHeld; ++u)
-        if (mine(w0 + u) && (pass == 0 || held_keys[u] >> (shift + L::kDigit) == T))
+        if (w0 + u < w1 && (pass == 0 || held_keys[u] >> (shift + L::kDigit) == T))
           atomicAdd(&h[(held_keys[u] >> shift) & (kBins - 1)], 1u);
       d = digit(pass);
       need = d.y;
@@ -343,15 +360,27 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
     }
     T <<= rest;
     cut = d.z != need;
+    uint32_t f = 0, e = 0;                               // lane u: those of word w0 + u
+    if (!cut) {
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const bool in = mine(w0 + u);
-      const uint32_t f = __ballot_sync(0xffffffffu, in && (cut ? held_keys[u] > T : held_keys[u] >= T));
-      const uint32_t e = __ballot_sync(0xffffffffu, in && cut && held_keys[u] == T);
-      if (lane == 0 && w0 + u < w1) {
-        flags[w0 + u] = f;
-        same[w0 + u] = e;
+      for (int u = 0; u < kHeld; ++u) {
+        const uint32_t v = __ballot_sync(0xffffffffu, held_keys[u] >= T);
+        if (lane == u) f = v;
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const uint32_t v = __ballot_sync(0xffffffffu, held_keys[u] > T);
+        const uint32_t z = __ballot_sync(0xffffffffu, held_keys[u] == T);
+        if (lane == u) {
+          f = v;
+          e = z;
+        }
+      }
+    }
+    if (lane < w1 - w0) {
+      flags[w0 + lane] = f;
+      same[w0 + lane] = e;
     }
   } else {
     uint32_t* h0 = hist_of(0);
@@ -457,10 +486,13 @@ __global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
         totals[2 * slot + 1] = ty;
       }
       cluster_sync();
-      for (int c = 0; c < rank; ++c) {
-        ix += ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot]), c));
-        iy += ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot + 1]), c));
+      tx = ty = 0;
+      if (lane < rank) {
+        tx = ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot]), lane));
+        ty = ld_cluster_u32(map_cluster(smem_addr(&totals[2 * slot + 1]), lane));
       }
+      ix += __reduce_add_sync(0xffffffffu, tx);
+      iy += __reduce_add_sync(0xffffffffu, ty);
     }
     return make_uint2(ix, iy);
   };

@@ -354,3 +354,20 @@ def test_offsets_beyond_32_bits(cuda_device):
     assert np.array_equal(weights[few, :, :97].cpu().numpy(), w1)
     assert np.array_equal(positions[few, :, :B].cpu().numpy(), p1[:, :, :B])
     assert (positions[:, :, B:] == -5).all() and (weights[:, :, 100:] == 7).all()
+
+
+def _few_numbers(rng, shape):
+    """Fewer numbers than the budget, the rest NaN: NaN's key decides."""
+    w = np.full(shape, np.nan, np.float32)
+    w[rng.random(shape) < 0.2] = 1.5
+    return w
+
+
+@pytest.mark.parametrize("ctx,Hk,budget,recorded", [
+    ((45, 333, 31), 2, 20, (0, 250, 0)), ((1101,) * 3, 1, 900, (900,) * 3),
+    ((5001, 4977), 1, 3000, None), ((60001, 33), 1, 20000, None),
+    ((333,) * 200, 1, 200, None), ((41, 570) * 100, 1, 30, None),
+], ids=["tiny", "steady", "registers", "streamed", "one_warp", "one_warp_18"])
+def test_select_where_nan_decides(ctx, Hk, budget, recorded, cuda_device):
+    b = Batch(cuda_device, ctx, Hk, budget, 99, recorded=recorded, weights=_few_numbers)
+    b.check_select(2, 11)
