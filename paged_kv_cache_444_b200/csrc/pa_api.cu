@@ -1278,7 +1278,7 @@ extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const f
   // and the tokens since the last eviction.  While all CTAs are resident, twice
   // the threads for half the words each (8 x 8 rows of 2065 slots: 12.3 -> 10.3 us;
   // 128 x 8 rows of 4113 took 59 us against 31; as the kernel is now, 6.5 and 19.4)
-  // of many rows each takes a single warp, if that holds its keys (106 x 32 rows of
+  // Of many rows each takes a single warp, if that holds its keys (106 x 32 rows of
   // 349 slots: 20.5 -> 13.7 us, 400 of 276: 8.1 -> 5.6; but two warps with 18
   // words for 128 x 8 rows of 1017: 14.9 against 12.1)
   if (run <= 32 * 9 && rows > sms)
@@ -1357,13 +1357,24 @@ namespace {
 // Workspace parts, each 256-byte aligned: tmp_out, part_m, part_l, logits.
 struct WeightsLayout {
   int64_t off[4];
-  int64_t total, parts;
+  int64_t total;
 };
+constexpr int64_t kWeightsCtas = 3 * 148;
 
+// Tokens of a partition: where the partitions would not fill the device (three
+// CTAs an SM), half or a quarter as many.
+int64_t weights_part(int64_t rows, int64_t cap) {
+  int64_t part = kWeightsPart;
+  while (part > kWeightsPartMin && rows * ((cap + part - 1) / part) < kWeightsCtas) part /= 2;
+  return part;
+}
+
+// The offsets hold for every num_kv_heads: for the smallest partitions, those of
+// 16 query heads a KV head.
 WeightsLayout weights_layout(int64_t S, int64_t H, int64_t D, int64_t MB, int64_t bs) {
   WeightsLayout l{};
-  l.parts = (MB * bs + kWeightsPart - 1) / kWeightsPart;
-  const int64_t rows = S * H * l.parts;
+  const int64_t part = weights_part((S * H + 15) / 16, MB * bs);
+  const int64_t rows = S * H * ((MB * bs + part - 1) / part);
   const int64_t sizes[4] = {rows * D * 4, rows * 4, rows * 4, S * H * MB * bs * 4};
   for (int i = 0; i < 4; ++i) {
     l.off[i] = l.total;
@@ -1377,12 +1388,8 @@ WeightsLayout weights_layout(int64_t S, int64_t H, int64_t D, int64_t MB, int64_
 // CTA's own last step to be small beside its pages.  128 x 8 contexts of 512 to
 // 4096 tokens: 207.6 us split, 198 single; 130 x 8 of 100 to 30000: 1338, 1297; but
 // 200 x 8 of up to 1000: 82, 90, and 112 x 8 of 4096 each (2.02 waves): 321, 333.
-#ifndef PA_WEIGHTS_SINGLE
-#define PA_WEIGHTS_SINGLE 6   // contexts an SM, at least (three CTAs are resident)
-#endif
-#ifndef PA_WEIGHTS_SINGLE_PARTS
-#define PA_WEIGHTS_SINGLE_PARTS 4   // partitions of the longest context, at least
-#endif
+constexpr int kWeightsSingle = 6;        // contexts an SM, at least (three CTAs are resident)
+constexpr int kWeightsSingleParts = 4;   // partitions of the longest context, at least
 
 template <int D, bool BF16, int NT>
 pa_status launch_weights_t(const CUtensorMap& km, const CUtensorMap& vm, const WeightsArgs& a,
@@ -1392,8 +1399,9 @@ pa_status launch_weights_t(const CUtensorMap& km, const CUtensorMap& vm, const W
   const long long rows = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
   const long long sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
-  if (a.parts == 1 ||
-      (rows >= PA_WEIGHTS_SINGLE * sms && a.parts >= PA_WEIGHTS_SINGLE_PARTS)) {
+  const long long cap = static_cast<long long>(a.max_blocks_per_seq) * kPage;
+  if (cap <= kWeightsPart ||
+      (rows >= kWeightsSingle * sms && cap > (kWeightsSingleParts - 1) * kWeightsPart)) {
     auto single = weights_single_kernel<D, NST, BF16, NT>;
     static std::atomic<uint64_t> done_single{0};
     if (!ensure_smem(single, L::kAlloc, &done_single)) return PA_ERR_CUDA;
@@ -1444,9 +1452,15 @@ extern "C" pa_status pa_decode_weights(void* out, float* weights, void* workspac
   const WeightsLayout l =
       weights_layout(num_seqs, num_heads, head_dim, max_blocks_per_seq, block_size);
   if (workspace_bytes < l.total) return PA_ERR_SHAPE;
-  const int64_t runs = (max_blocks_per_seq * block_size + kWeightsRun - 1) / kWeightsRun;
-  const int64_t items = num_seqs * num_kv_heads * l.parts;
-  const int64_t merge = num_seqs * num_kv_heads * runs;
+  const int64_t rows = num_seqs * num_kv_heads, cap = max_blocks_per_seq * block_size;
+  const int64_t group = num_heads / num_kv_heads, part = weights_part(rows, cap);
+  const int64_t parts = (cap + part - 1) / part;
+  // tokens of a second-pass CTA: 16384 logits, fewer while there are few CTAs
+  int64_t run = kWeightsRun;
+  while (run > 256 && (run * group > 16384 || rows * ((cap + run - 1) / run) < kWeightsCtas))
+    run /= 2;
+  const int64_t runs = (cap + run - 1) / run;
+  const int64_t items = rows * parts, merge = rows * runs;
   if (items > INT32_MAX || merge > INT32_MAX) return PA_ERR_SHAPE;
   CUtensorMap km, vm;
   if (!encode_cache_map(&km, key_cache, dtype, num_blocks, num_kv_heads, head_dim) ||
@@ -1472,7 +1486,9 @@ extern "C" pa_status pa_decode_weights(void* out, float* weights, void* workspac
   a.num_blocks = static_cast<int>(num_blocks);
   a.max_tokens = static_cast<int>(max_tokens);
   a.new_tokens = static_cast<int>(new_tokens);
-  a.parts = static_cast<int>(l.parts);
+  a.part = static_cast<int>(part);
+  a.run = static_cast<int>(run);
+  a.parts = static_cast<int>(parts);
   a.runs = static_cast<int>(runs);
   cudaStream_t s = as_stream(stream);
   const bool bf16 = dtype == PA_BF16, wide = a.group > 8;

@@ -10,7 +10,7 @@
 // small pass turns them into weights.
 //
 //   weights_split_kernel  one CTA per (sequence, KV head, partition of
-//     kWeightsPart tokens): the page pipeline and the transposed page step of
+//     up to kWeightsPart tokens): the page pipeline and the transposed page step of
 //     the split decode (tokens and head dims as the mma's rows, heads as its
 //     columns, one or two column tiles of 8), with the logits written out.
 //   weights_merge_kernel  a CTA per (sequence, KV head, run of tokens) finds the
@@ -23,6 +23,9 @@
 // the second pass reads them: it reads 4 MB of its 58 from DRAM, and costs the
 // call another 15 us, most of it latency at the first pass's end.  8 sequences of
 // 32768 to 131072 tokens: 460 us, the second pass 35 of them.
+// Few rows take smaller partitions and runs: 64 contexts of 1368 to 4104 tokens,
+// 16 heads over one, 29 us instead of 51; 28 of 1899 18 instead of 26; 11 of 390 to
+// 3125, 4 heads of 64, 11 instead of 17.
 //
 //   weights_single_kernel  both in one, a CTA per (sequence, KV head), where there
 //     are enough of those: the CTA knows its heads' lse at the end of its own
@@ -33,8 +36,9 @@
 
 namespace pa {
 
-constexpr int kWeightsPart = 512;          // tokens per partition
-constexpr int kWeightsRun = 4096;          // tokens per CTA of the second pass
+constexpr int kWeightsPart = 512;          // tokens per partition, at most
+constexpr int kWeightsPartMin = 128;       // and at least
+constexpr int kWeightsRun = 4096;          // tokens per CTA of the second pass, at most
 constexpr int kWeightsThreads = 256;
 constexpr int kWeightsBatch = 4;           // tokens (or partitions of O) loaded before any is used
 
@@ -57,6 +61,8 @@ struct WeightsArgs {
   int num_blocks;
   int max_tokens;
   int new_tokens;
+  int part;                      // tokens of a partition
+  int run;                       // tokens of a second-pass CTA
   int parts;                     // P
   int runs;                      // CTAs per (sequence, KV head) that add weights up
 };
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0 && part == 0 && kvh == 0) record_error(kErrContextLen, s);
     ctx = ctx < 0 ? 0 : cap;
   }
-  const int t_begin = part * kWeightsPart, t_end = min(t_begin + kWeightsPart, ctx);
+  const int t_begin = part * a.part, t_end = min(t_begin + a.part, ctx);
   if (t_begin >= t_end) return;
   const int group = a.group;
   const int first_page = t_begin / kPage;
@@ -353,34 +359,63 @@ __global__ void __launch_bounds__(kThreads)
 
 // weights[t] += sum_g 2^(z_tg - lse_g) for tokens t0 <= t < t1 (set from `fresh`
 // on), by the kThreadsN threads of a CTA, kWeightsBatch tokens a thread at a time.
+// Four heads a load: Q lanes share a token, so that a warp's loads are one piece.
+// One such step from token b0; kWhole: all its tokens are before t1 and not new.
+template <int kThreadsN, int Q, bool kWhole>
+__device__ __forceinline__ void add_step_by_four(const float* z, float* w, int b0, int t1,
+                                                 int fresh, int G, const float* lse_sh, int tid) {
+  constexpr int kTokens = kThreadsN / Q;
+  const int sub = tid % Q, first = b0 + tid / Q;
+  float sum[kWeightsBatch], old[kWeightsBatch];
+#pragma unroll
+  for (int u = 0; u < kWeightsBatch; ++u) {
+    const int t = first + u * kTokens;
+    sum[u] = 0.f;
+    old[u] = sub == 0 && (kWhole || (t < t1 && t < fresh)) ? w[t] : 0.f;
+  }
+  const float* zt = z + static_cast<size_t>(first) * G;
+  for (int g = 4 * sub; g < G; g += 4 * Q) {
+    const float4 l = *reinterpret_cast<const float4*>(lse_sh + g);
+    float4 v[kWeightsBatch];
+#pragma unroll
+    for (int u = 0; u < kWeightsBatch; ++u)
+      v[u] = kWhole || first + u * kTokens < t1
+                 ? *reinterpret_cast<const float4*>(zt + u * kTokens * G + g)
+                 : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll
+    for (int u = 0; u < kWeightsBatch; ++u)
+      sum[u] += (ex2(v[u].x - l.x) + ex2(v[u].y - l.y)) +
+                (ex2(v[u].z - l.z) + ex2(v[u].w - l.w));
+  }
+#pragma unroll
+  for (int u = 0; u < kWeightsBatch; ++u) {
+#pragma unroll
+    for (int o = 1; o < Q; o <<= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+    const int t = first + u * kTokens;
+    if (sub == 0 && (kWhole || t < t1)) w[t] = old[u] + sum[u];
+  }
+}
+
+template <int kThreadsN, int Q>
+__device__ __forceinline__ void add_weights_by_four(const float* z, float* w, int t0, int t1,
+                                                    int fresh, int G, const float* lse_sh,
+                                                    int tid) {
+  constexpr int kStep = kThreadsN / Q * kWeightsBatch;
+  int b0 = t0;
+  for (; b0 + kStep <= min(t1, fresh); b0 += kStep)
+    add_step_by_four<kThreadsN, Q, true>(z, w, b0, t1, fresh, G, lse_sh, tid);
+  for (; b0 < t1; b0 += kStep)
+    add_step_by_four<kThreadsN, Q, false>(z, w, b0, t1, fresh, G, lse_sh, tid);
+}
+
 template <int kThreadsN>
 __device__ __forceinline__ void add_weights(const float* z, float* w, int t0, int t1, int fresh,
                                             int G, const float* lse_sh, int tid) {
+  if (G == 16) return add_weights_by_four<kThreadsN, 4>(z, w, t0, t1, fresh, G, lse_sh, tid);
+  if (G == 8) return add_weights_by_four<kThreadsN, 2>(z, w, t0, t1, fresh, G, lse_sh, tid);
+  if ((G & 3) == 0) return add_weights_by_four<kThreadsN, 1>(z, w, t0, t1, fresh, G, lse_sh, tid);
   constexpr int kStep = kThreadsN * kWeightsBatch;
   for (int b0 = t0; b0 < t1; b0 += kStep) {
-    // whole batches of tokens that are not new need no checks, and take four
-    // heads a load
-    if ((G & 3) == 0 && b0 + kStep <= min(t1, fresh)) {
-      const float4* zt = reinterpret_cast<const float4*>(z + static_cast<size_t>(b0 + tid) * G);
-      float* wt = w + b0 + tid;
-      float sum[kWeightsBatch];
-#pragma unroll
-      for (int u = 0; u < kWeightsBatch; ++u) sum[u] = wt[u * kThreadsN];
-      for (int g = 0; g < G; g += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(lse_sh + g);
-        float4 v[kWeightsBatch];
-#pragma unroll
-        for (int u = 0; u < kWeightsBatch; ++u)
-          v[u] = zt[(u * kThreadsN * G + g) >> 2];
-#pragma unroll
-        for (int u = 0; u < kWeightsBatch; ++u)
-          sum[u] += (ex2(v[u].x - l.x) + ex2(v[u].y - l.y)) +
-                    (ex2(v[u].z - l.z) + ex2(v[u].w - l.w));
-      }
-#pragma unroll
-      for (int u = 0; u < kWeightsBatch; ++u) wt[u * kThreadsN] = sum[u];
-      continue;
-    }
     float sum[kWeightsBatch] = {};
     for (int g = 0; g < G; ++g) {
       float v[kWeightsBatch];
@@ -571,9 +606,9 @@ __global__ void __launch_bounds__(kWeightsThreads)
   const int run = blockIdx.x % a.runs, row = blockIdx.x / a.runs;   // row = s * Hk + kv
   const int s = row / a.num_kv_heads, kv = row % a.num_kv_heads;
   const int ctx = min(max(a.context_lens[s], 0), cap);
-  const int t0 = run * kWeightsRun, t1 = min(t0 + kWeightsRun, ctx);
+  const int t0 = run * a.run, t1 = min(t0 + a.run, ctx);
   if (t0 >= t1 && run > 0) return;
-  const int np = (ctx + kWeightsPart - 1) / kWeightsPart;
+  const int np = (ctx + a.part - 1) / a.part;
   const int G = a.group;
   const size_t hrow = static_cast<size_t>(s) * a.num_heads + kv * G;
   for (int g = warp; g < G; g += kWarpsM) {
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(kWeightsThreads)
   }
 
   // ---- this run's share of the heads' outputs, a row a warp or several ----
-  const int live_runs = max(1, (ctx + kWeightsRun - 1) / kWeightsRun);
+  const int live_runs = max(1, (ctx + a.run - 1) / a.run);
   const int per = (G + live_runs - 1) / live_runs;
   const int g0 = min(run * per, G), g1 = min(g0 + per, G);
   // a row's partitions over `share` warps, so that few rows keep all warps busy

@@ -62,6 +62,8 @@ CASES = {
     "tiny": ((1, 9, 16, 37), 4, 4, 64, "f16", 1, 3),
     "empty_between": ((0, 17, 0, 33), 8, 2, 128, "bf16", 1, 1),
     "partition_edges": ((511, 512, 513, 1023, 1025), 8, 2, 128, "bf16", 1, 7),
+    "small_partition_edges": ((127, 128, 129, 255, 257, 640), 8, 2, 128, "bf16", 1, 7),
+    "small_partitions_group16": ((1281, 100, 256, 0), 16, 1, 64, "f16", 3, 0),
     "group3": ((45, 700), 12, 4, 128, "f16", 1, 0),
     "group2_bf16_d64": ((130, 1), 4, 2, 64, "bf16", 1, 5),
     "group8": ((600, 31), 16, 2, 128, "f16", 2, 0),
