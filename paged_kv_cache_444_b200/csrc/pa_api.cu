@@ -1456,6 +1456,7 @@ extern "C" pa_status pa_decode_weights(void* out, float* weights, void* workspac
   const int64_t group = num_heads / num_kv_heads, part = weights_part(rows, cap);
   const int64_t parts = (cap + part - 1) / part;
   // tokens of a second-pass CTA: 16384 logits, fewer while there are few CTAs
+  // (with 2048 instead of 4096 at four heads the long contexts take 470 us, not 467)
   int64_t run = kWeightsRun;
   while (run > 256 && (run * group > 16384 || rows * ((cap + run - 1) / run) < kWeightsCtas))
     run /= 2;
@@ -1559,17 +1560,33 @@ pa_status check_prompt_rows(const void* rows, int64_t stride, int64_t width) {
   return PA_OK;
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool kHalves>
 pa_status launch_prompt_t(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                           const PromptArgs& a, long long items, cudaStream_t stream) {
   using L = PromptSmem<D>;
-  auto kernel = prompt_attention_kernel<D, BF16>;
+  auto kernel = prompt_attention_kernel<D, BF16, kHalves>;
   static std::atomic<uint64_t> done{0};
   if (!ensure_smem(kernel, L::kAlloc, &done)) return PA_ERR_CUDA;
   const long long sms = sm_count();
   if (sms <= 0) return PA_ERR_CUDA;
   return launch_ex(kernel, static_cast<unsigned>(items < sms ? items : sms), kPromptThreads,
                    L::kAlloc, stream, 1, qm, km, vm, a);
+}
+// Where there are fewer pairs of tiles than SMs, an item is one tile, its even key
+// blocks and its odd ones (1976 tokens, 12 heads over 4, 96 pairs: 38.0 us with
+// pairs, 26.6; 4000 of 8 over 1, 126 pairs: 65 and 42; but 3500 of 16 over 4, 220
+// pairs: 59 and 65, for every K and V block is loaded for half as many rows).
+template <int D, bool BF16>
+pa_status launch_prompt_rows(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                             const PromptArgs& a, long long items, cudaStream_t stream) {
+  const long long sms = sm_count();
+  if (sms <= 0) return PA_ERR_CUDA;
+  if (items <= sms) {
+    const long long tiles =
+        (static_cast<long long>(a.num_tokens) / a.tile_tokens + a.num_seqs) * a.num_kv_heads;
+    return launch_prompt_t<D, BF16, true>(qm, km, vm, a, tiles, stream);
+  }
+  return launch_prompt_t<D, BF16, false>(qm, km, vm, a, items, stream);
 }
 }  // namespace
 
@@ -1617,10 +1634,10 @@ extern "C" pa_status pa_prompt_attention(void* out, float* lse, const void* quer
   cudaStream_t s = as_stream(stream);
   const bool bf16 = dtype == PA_BF16;
   if (head_dim == 64)
-    return bf16 ? launch_prompt_t<64, true>(qm, km, vm, a, items, s)
-                : launch_prompt_t<64, false>(qm, km, vm, a, items, s);
-  return bf16 ? launch_prompt_t<128, true>(qm, km, vm, a, items, s)
-              : launch_prompt_t<128, false>(qm, km, vm, a, items, s);
+    return bf16 ? launch_prompt_rows<64, true>(qm, km, vm, a, items, s)
+                : launch_prompt_rows<64, false>(qm, km, vm, a, items, s);
+  return bf16 ? launch_prompt_rows<128, true>(qm, km, vm, a, items, s)
+              : launch_prompt_rows<128, false>(qm, km, vm, a, items, s);
 }
 // <<< whole-prompt attention
 

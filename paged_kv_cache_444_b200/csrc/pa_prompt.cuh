@@ -23,6 +23,10 @@
 // phase running on from item to item.  Warps: 0-3 and 4-7 the softmax of tiles
 // A and B, 8 issues the MMAs, 9 the loads, 10-11 look through V.
 //
+// With few tiles (kHalves) an item is one tile, and A and B are its even and its
+// odd key blocks, each with its own m, l and O; the epilogue joins them, each
+// warpgroup half of the columns.  Twice the items, half as long.
+//
 // A key that a row does not see has p = 0, but 0 times a NaN or an infinite
 // value is NaN.  Only a block that holds such a key for some row (the diagonal,
 // the sequence's end) can carry one over, so warps 10-11 look through those
@@ -90,6 +94,10 @@ struct PromptSmem {
   static constexpr int kBarQFree = kBarEnd + 8;          // an item's S products done
   static constexpr int kBarOFull = kBarQFree + 8;        // per tile: an item's last P V done
   static constexpr int kBarOFree = kBarOFull + 16;       // per tile: O read by the epilogue
+  // one tile in two halves: the halves' m and l are in, and where they are (the
+  // second tile's Q has no use then)
+  static constexpr int kBarHalves = kBarOFree + 8;
+  static constexpr int kHalfStats = kQ + kQTile;
   static constexpr int kTmemSlot = kBarOFree + 16;
   static constexpr int kAbort = kTmemSlot + 4;
   static constexpr int kMark = kAbort + 4;               // a V value that is not finite was met
@@ -290,9 +298,11 @@ __device__ __forceinline__ PromptUnit prompt_unit(const Args& a, const PromptOrd
 }
 
 struct PromptItem {
-  int s, kvh, q0, len, tile_a, lim[2], nkb[2];   // keys each tile's last token sees, their blocks
+  int s, kvh, q0, len, tile_a, blocks;   // key blocks of the item
+  int lim[2], nkb[2];                    // keys each tile's last token sees, its blocks
 };
 
+template <bool kHalves>
 __device__ __forceinline__ void prompt_item(const PromptArgs& a, const PromptOrder& o,
                                             const int4* seqs, const int* list, int i, int span,
                                             PromptItem& it) {
@@ -303,11 +313,19 @@ __device__ __forceinline__ void prompt_item(const PromptArgs& a, const PromptOrd
   it.q0 = unit.q0;
   it.len = unit.len;
   it.tile_a = unit.pair * span;
+  if constexpr (kHalves) {   // one tile, its even and its odd blocks
+    it.lim[0] = it.lim[1] = min(it.tile_a + span, it.len);
+    it.blocks = (it.lim[0] + kPrefillKeys - 1) / kPrefillKeys;
+    it.nkb[0] = (it.blocks + 1) / 2;
+    it.nkb[1] = it.blocks / 2;
+    return;
+  }
   const int half = span / 2;
   it.lim[0] = min(it.tile_a + half, it.len);
   it.lim[1] = it.tile_a + half < it.len ? min(it.tile_a + span, it.len) : 0;
   it.nkb[0] = (it.lim[0] + kPrefillKeys - 1) / kPrefillKeys;
   it.nkb[1] = (it.lim[1] + kPrefillKeys - 1) / kPrefillKeys;
+  it.blocks = max(it.nkb[0], it.nkb[1]);
 }
 
 // One 128-key block of a tile's online softmax, thread = row: S (fp32, in p)
@@ -385,7 +403,7 @@ __device__ __forceinline__ void prompt_softmax_block(float (&p)[kPrefillKeys], b
   tmem_wait_st();
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool kHalves>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap qmap,
                             const __grid_constant__ CUtensorMap kmap,
@@ -405,7 +423,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   pdl_launch_dependents();
   pdl_wait();
 
-  const int G = a.group, span = 2 * a.tile_tokens;
+  const int G = a.group, span = kHalves ? a.tile_tokens : 2 * a.tile_tokens;
   int4* seqs = reinterpret_cast<int4*>(smem + L::kSeqs);
   int* list = reinterpret_cast<int*>(smem + L::kList);
   const PromptOrder order = prompt_order(a, span, reinterpret_cast<int*>(smem + L::kSched), seqs,
@@ -430,7 +448,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(sb + L::kBarS + 8 * t, 1);
       mbar_init(sb + L::kBarP + 8 * t, 128);
       mbar_init(sb + L::kBarOFull + 8 * t, 1);
-      mbar_init(sb + L::kBarOFree + 8 * t, 128);
+      mbar_init(sb + L::kBarOFree + 8 * t, kHalves ? 256 : 128);
     }
     mbar_init(sb + L::kBarEnd, 1);
     *abort_flag = 0;
@@ -463,10 +481,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
         if (i < 0) break;
         PromptItem it;
-        prompt_item(a, order, seqs, list, i, span, it);
+        prompt_item<kHalves>(a, order, seqs, list, i, span, it);
         // the first K block goes ahead of Q, which has to wait for the last
         // item's S products
-        const int nkb = max(it.nkb[0], it.nkb[1]);
+        const int nkb = it.blocks;
         for (int j = 0; j < nkb; ++j, ++issued) {
           const int st = issued % NST;
           const uint32_t par = ((issued / NST) & 1) ^ 1;
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                  sb + L::kBarQFree, (n_q - 1) & 1, abort_flag))))
               break;
             if (lane == 0) {
-              const int tiles = it.lim[1] > 0 ? 2 : 1;
+              const int tiles = !kHalves && it.lim[1] > 0 ? 2 : 1;
               mbar_arrive_expect_tx(sb + L::kBarQ, tiles * L::kSlabs * q_rows * 128);
               for (int t = 0; t < tiles; ++t) {
 #pragma unroll
@@ -532,7 +550,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const uint64_t vdesc = umma_desc_sw128(sb + L::kV, L::kSlab, 1024);
       const bool leader = elect_lane();
       auto issue_s = [&](int t, int st) {
-        const uint64_t q = qdesc + t * (L::kQTile / 16), kd = kdesc + st * kStage16;
+        const uint64_t q = qdesc + (kHalves ? 0 : t * (L::kQTile / 16)), kd = kdesc + st * kStage16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * L::kSlab + (kk & 3) * 32) / 16;
@@ -568,10 +586,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
         if (i < 0) break;
         PromptItem it;
-        prompt_item(a, order, seqs, list, i, span, it);
+        prompt_item<kHalves>(a, order, seqs, list, i, span, it);
         const int nkb[2] = {warp_uniform(it.nkb[0]), warp_uniform(it.nkb[1])};
         const int lim[2] = {warp_uniform(it.lim[0]), warp_uniform(it.lim[1])};
-        const int blocks = max(nkb[0], nkb[1]);
+        const int blocks = warp_uniform(it.blocks);
         // P_t of block j (stage vs) is in: its product, after the epilogue has
         // read the last item's O_t
         auto pv = [&](int t, int j, int vs) {
@@ -587,6 +605,50 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         if (!(ok = wait(sb + L::kBarQ, n_q & 1))) break;
         ++n_q;
+        if constexpr (kHalves) {
+          // S(j) by the half j & 1, then P(j - 1) V by the other
+          int last = 0, last_par = 0;
+          for (int j = 0; j <= blocks; ++j) {
+            if (j < blocks) {
+              if (!(ok = wait(sb + L::kBarKFull + 8 * st, par))) break;
+              if (leader) {
+                if (j & 1) issue_s(1, st);
+                else issue_s(0, st);
+                umma_commit(sb + L::kBarKEmpty + 8 * st);
+                if (j == blocks - 1) umma_commit(sb + L::kBarQFree);
+              }
+              __syncwarp();
+            }
+            if (j > 0) {
+              const int t = (j - 1) & 1, r = (j - 1) >> 1;
+              if (!(ok = wait(sb + L::kBarVOk + 8 * last, last_par))) break;
+              // (both epilogue halves free both accumulators at once)
+              if (r == 0 && items[0] > 0 &&
+                  !(ok = wait(sb + L::kBarOFree, (items[0] - 1) & 1)))
+                break;
+              if (!(ok = wait(sb + L::kBarP + 8 * t, (done[t] + r) & 1))) break;
+              if (leader) {
+                const int keys = lim[0] - (j - 1) * kPrefillKeys;
+                if (t) issue_pv(1, last, r == 0, keys);
+                else issue_pv(0, last, r == 0, keys);
+                umma_commit(sb + L::kBarVEmpty + 8 * last);
+                if (r == nkb[t] - 1) umma_commit(sb + L::kBarOFull + 8 * t);
+              }
+              __syncwarp();
+            }
+            last = st;
+            last_par = par;
+            if (j < blocks && ++st == NST) {
+              st = 0;
+              par ^= 1;
+            }
+          }
+          if (!ok) break;
+          done[0] += nkb[0];
+          done[1] += nkb[1];
+          ++items[0];
+          continue;
+        }
         if (!(ok = wait(sb + L::kBarKFull + 8 * st, par))) break;
         int last = 0;                      // the stage of the block before
         for (int j = 0; j <= blocks && ok; ++j) {
@@ -635,8 +697,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
         if (i < 0) break;
         PromptItem it;
-        prompt_item(a, order, seqs, list, i, span, it);
-        const int nkb = max(it.nkb[0], it.nkb[1]);
+        prompt_item<kHalves>(a, order, seqs, list, i, span, it);
+        const int nkb = it.blocks;
         for (int j = 0; j < nkb; ++j) {
           const int g = g0 + j, st = g % NST;
           if (!(ok = __all_sync(0xffffffffu, wait_or_abort(sb + L::kBarVFull + 8 * st,
@@ -677,17 +739,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_addr = t_lane + kTmemS + 128 * t, o_addr = t_lane + kTmemO + 128 * t;
     const float sl2 = a.scale_log2;
-    int done = 0, items = 0;
+    int done = 0, items = 0, twos = 0;   // twos: items with blocks for both halves
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int i = prefill_item_index(k, total, blockIdx.x, gridDim.x);
       if (i < 0) break;
       PromptItem it;
-      prompt_item(a, order, seqs, list, i, span, it);
+      prompt_item<kHalves>(a, order, seqs, list, i, span, it);
       if (it.lim[t] == 0) continue;
-      const int tok = it.tile_a + t * a.tile_tokens + row / G;    // this row's token
+      const int tok0 = it.tile_a + (kHalves ? 0 : t * a.tile_tokens);
+      const int tok = tok0 + row / G;                             // this row's token
       const bool live = row < q_rows && tok < it.len;
-      const int lim = live ? tok + 1 : it.nkb[t] * kPrefillKeys;   // (what a row of no token holds is not written)
+      const int lim = live ? tok + 1 : it.blocks * kPrefillKeys;   // (what a row of no token holds is not written)
       float m = -INFINITY, l = 0.f;
       const int nkb = it.nkb[t];
       for (int j = 0; j < nkb; ++j) {
@@ -698,35 +761,67 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tmem_fence_after_sync();
         float p[kPrefillKeys];
         tmem_ld128_x32(s_addr, p);
-        prompt_softmax_block<BF16, D>(p, j == 0, lim - j * kPrefillKeys, sl2, m, l, s_addr,
+        prompt_softmax_block<BF16, D>(p, j == 0,
+                                      lim - (kHalves ? 2 * j + t : j) * kPrefillKeys, sl2, m, l, s_addr,
                                       o_addr);
         tmem_fence_before_sync();
         mbar_arrive(sb + L::kBarP + 8 * t);
       }
       if (!ok) break;
       done += nkb;
-      ok = __all_sync(0xffffffffu, wait_or_abort(sb + L::kBarOFull + 8 * t, items & 1,
+      const int of = kHalves ? 0 : t;
+      ok = __all_sync(0xffffffffu, wait_or_abort(sb + L::kBarOFull + 8 * of, items & 1,
                                                  abort_flag));
       if (!ok) break;
+      // Both halves are in: each takes half of the columns of
+      // O = 2^(m_a - m) O_a + 2^(m_b - m) O_b, from the same lanes of tensor memory
+      float fa = 1.f, fb = 0.f;
+      const bool two = kHalves && it.nkb[1] > 0;
+      if constexpr (kHalves) {
+        if (two && !(ok = __all_sync(0xffffffffu, wait_or_abort(sb + L::kBarOFull + 8, twos & 1,
+                                                                abort_flag))))
+          break;
+        // (the exchange's last readers arrived at OFree before this item's products began)
+        float2* ml = reinterpret_cast<float2*>(smem + L::kHalfStats);
+        ml[128 * t + row] = make_float2(m, l);
+        mbar_arrive(sb + L::kBarHalves);
+        ok = __all_sync(0xffffffffu, wait_or_abort(sb + L::kBarHalves, items & 1, abort_flag));
+        if (!ok) break;
+        const float2 ha = ml[row], hb = ml[128 + row];
+        m = fmaxf(ha.x, hb.x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        fa = ex2(ha.x - ref);
+        fb = ex2(hb.x - ref);
+        l = fa * ha.y + fb * hb.y;
+      }
       // ---- O / l, and the log-sum-exp ----
       tmem_fence_after_sync();
       const bool marked = *mark != 0;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN stays one
       const size_t hrow = static_cast<size_t>(it.q0 + tok) * a.num_heads + it.kvh * G + row % G;
-      if (live && a.lse) a.lse[hrow] = m * kLn2 + logf(l);
+      if (live && a.lse && (!kHalves || t == 0)) a.lse[hrow] = m * kLn2 + logf(l);
       // 32 columns at a time through shared memory (16-byte chunk c of row r at
       // c ^ (r / 2 % 4), free of bank conflicts), so that four lanes store a row's
       // 64 bytes: a lane a row touched 32 lines a store, and the epilogue took
       // 3700 to 6000 cycles an item
       const uint32_t stage = sb + L::kStore + warp * 2048;
       const int r0 = warp & 3;                         // this warp's rows: 32 r0 ..
+      const int c_end = kHalves ? (t + 1) * (D / 64) : D / 32;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = kHalves ? t * (D / 64) : 0; c < c_end; ++c) {
         float o[32];
-        tmem_ld32(o_addr + 32 * c, o);
-        if (c == D / 32 - 1) {                         // O_t is in registers
+        tmem_ld32((kHalves ? t_lane + kTmemO : o_addr) + 32 * c, o);
+        if constexpr (kHalves) {
+          if (two) {
+            float b[32];
+            tmem_ld32(t_lane + kTmemO + 128 + 32 * c, b);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = fa * o[q] + fb * b[q];
+          }
+        }
+        if (c == c_end - 1) {                          // O_t is in registers
           tmem_fence_before_sync();
-          mbar_arrive(sb + L::kBarOFree + 8 * t);
+          mbar_arrive(sb + L::kBarOFree + 8 * of);
         }
         if (marked && live) {
           // what the guard took out, for the keys this row sees
@@ -755,7 +850,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                        : "r"(stage + r * 64 + ((ch ^ (r >> 1 & 3)) << 4)));
-          const int rt = it.tile_a + t * a.tile_tokens + tr / G;
+          const int rt = tok0 + tr / G;
           if (tr < q_rows && rt < it.len)
             *reinterpret_cast<uint4*>(a.out +
                 (static_cast<size_t>(it.q0 + rt) * a.num_heads + it.kvh * G + tr % G) * D +
@@ -763,6 +858,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
       ++items;
+      twos += two;
     }
   }
 

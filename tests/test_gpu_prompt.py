@@ -78,6 +78,10 @@ CASES = {
     "mha_f16": ((200, 65, 129), 4, 4, 128, "f16", dict(fused=True)),
     "ragged_gqa4": ((513, 77, 1210, 640), 8, 2, 128, "bf16", dict(fused=True, trail=11)),
     "long_gqa8_d64": ((2500, 1100), 8, 1, 64, "f16", {}),
+    # more pairs of tiles than SMs: two tiles an item (else one, in two halves)
+    "pairs_mha_d64": ((2500, 1100, 700), 16, 16, 64, "f16", dict(trail=2)),
+    "pairs_gqa4": ((1300, 900, 513), 32, 8, 128, "bf16", dict(fused=True, lead=3)),
+    "pairs_group3": ((300, 41, 84, 85), 48, 16, 128, "f16", {}),
     "long_mha": ((1900, 1025), 2, 2, 128, "bf16", {}),
 }
 
@@ -109,9 +113,10 @@ def test_many_sequences(lens, H, Hk, seqs, cuda_device):
 def test_other_scales(scale, dtype, cuda_device):
     """1: peaked rows whose reference maximum moves between the key blocks."""
     Prompt(cuda_device, (900, 333), 8, 2, 128, dtype, 82).run(scale).check()
+    Prompt(cuda_device, (900, 333), 32, 16, 128, dtype, 92).run(scale).check(heads=[0, 9, 31])
 
 
-@pytest.mark.parametrize("H,Hk,dtype", [(2, 2, "bf16"), (8, 2, "f16")])
+@pytest.mark.parametrize("H,Hk,dtype", [(2, 2, "bf16"), (8, 2, "f16"), (32, 32, "bf16")])
 def test_climbing_logits(H, Hk, dtype, cuda_device):
     """Logits that climb by 10 log2 units every 64 keys, for half of the rows."""
     p = Prompt(cuda_device, (700, 100), H, Hk, 128, dtype, 83)
@@ -123,7 +128,8 @@ def test_climbing_logits(H, Hk, dtype, cuda_device):
     p.run().check()
 
 
-@pytest.mark.parametrize("dtype,H,Hk,D", [("bf16", 8, 2, 128), ("f16", 2, 2, 64)])
+@pytest.mark.parametrize("dtype,H,Hk,D", [("bf16", 8, 2, 128), ("f16", 2, 2, 64),
+                                            ("bf16", 64, 16, 128)])
 def test_what_a_token_does_not_see_does_not_reach_it(dtype, H, Hk, D, cuda_device):
     """NaN and infinities in a later token's rows and in the next sequence's."""
     p = Prompt(cuda_device, (150, 90, 40, 260), H, Hk, D, dtype, 84)
