@@ -443,15 +443,21 @@ __global__ void __launch_bounds__(kPwThreads, 1)
       }
       if (!ok) break;
       n += it.tiles;
-      // the odd tiles' sums go to the even tiles' warpgroup.  Two items' sums
-      // alternate: a thread that writes those of the item after next has passed
-      // the barrier of the next one, which every reader of this one's reaches later.
+      // the odd tiles' sums go to the even tiles' warpgroup, and their own goes on to
+      // the next item.  Two items' sums alternate: whoever writes those of the item
+      // after next has waited for the next one's barrier, which the readers of this
+      // one's reach later.
       float* part = sums + (items & 1) * kPwSpan;
-      if (h == 1) part[128 * b + key] = acc;
+      if (h == 1) {
+        if (items > 0 && !(ok = wait(sb + L::kBarSums, (items - 1) & 1))) break;
+        part[128 * b + key] = acc;
+        mbar_arrive(sb + L::kBarSums);
+        ++items;
+        continue;
+      }
       mbar_arrive(sb + L::kBarSums);
       if (!(ok = wait(sb + L::kBarSums, items & 1))) break;
       ++items;
-      if (h == 1) continue;
       float sum = acc + part[128 * b + key];
       if (C > 1) {
         // slot: of two items; use: how often it has been used before
