@@ -156,6 +156,7 @@ def _need(cond: bool, msg: str) -> None:
 # The handle of a device's current stream, without the Stream object around it
 # (3 us a call, as much as a launch).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_on_one_device(stream, *tensors) -> int:
@@ -163,13 +164,15 @@ def _stream_on_one_device(stream, *tensors) -> int:
     every tensor must be there (and the stream, when it is a torch stream)."""
     dev = tensors[0].get_device()       # -1: host memory
     for t in tensors:
-        if t.get_device() != dev or dev < 0:
+        if t.get_device() != dev:
             raise ValueError("tensors must be on one CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev < 0:
+        raise ValueError("tensors must be on one CUDA device")
+    if dev != _current_device():
         raise ValueError("tensors must be on the current device")
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(dev)
-    if stream is not None and hasattr(stream, "device") and stream.device.index != dev:
+    if stream is None:
+        return _stream(None) if _raw_stream is None else _raw_stream(dev)
+    if hasattr(stream, "device") and stream.device.index != dev:
         raise ValueError("stream and tensors must be on one device")
     return _stream(stream)
 
@@ -410,10 +413,11 @@ def _prompt_rows(name, rows, T, D):
 
 def _prompt_starts(seq_starts):
     """The number of sequences."""
-    _need(seq_starts.dtype == torch.int32 and seq_starts.dim() == 1 and
-          seq_starts.shape[0] >= 1 and seq_starts.is_contiguous(),
-          "seq_starts must be [num_seqs + 1] int32")
-    return seq_starts.shape[0] - 1
+    shape = seq_starts.shape
+    if (seq_starts.dtype != torch.int32 or len(shape) != 1 or shape[0] < 1 or
+            not seq_starts.is_contiguous()):
+        raise ValueError("seq_starts must be [num_seqs + 1] int32")
+    return shape[0] - 1
 
 
 def _weights_columns(weights, S, Hk):
@@ -437,17 +441,19 @@ def pa_prompt_attention(out: torch.Tensor, lse: torch.Tensor | None, query: torc
     ks = _prompt_rows("key", key, T, D)
     vs = _prompt_rows("value", value, T, D)
     Hk = key.shape[1]
-    _need(value.shape[1] == Hk, "key/value shapes differ")
-    _need(key.dtype == dtype and value.dtype == dtype, "dtype mismatch")
-    _need(out.shape == shape and out.dtype == dtype and out.is_contiguous(),
-          "out must be [num_tokens, num_heads, head_dim] contiguous")
+    if value.shape[1] != Hk:
+        raise ValueError("key/value shapes differ")
+    if key.dtype != dtype or value.dtype != dtype:
+        raise ValueError("dtype mismatch")
+    if out.shape != shape or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError("out must be [num_tokens, num_heads, head_dim] contiguous")
     S = _prompt_starts(seq_starts)
     dt = _dtype_code(query)
     if lse is None:
         at, s = None, _stream_on_one_device(stream, query, key, value, out, seq_starts)
     else:
-        _need(lse.dtype == torch.float32 and lse.shape == shape[:2] and lse.is_contiguous(),
-              "lse must be [num_tokens, num_heads] float32")
+        if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be [num_tokens, num_heads] float32")
         at = lse.data_ptr()
         s = _stream_on_one_device(stream, query, key, value, out, seq_starts, lse)
     st = load().pa_prompt_attention(out.data_ptr(), at, query.data_ptr(), key.data_ptr(),
@@ -467,9 +473,10 @@ def pa_prompt_weights(weights: torch.Tensor, query: torch.Tensor, key: torch.Ten
     qs = _prompt_rows("query", query, T, D)
     ks = _prompt_rows("key", key, T, D)
     Hk = key.shape[1]
-    _need(query.dtype == key.dtype, "dtype mismatch")
-    _need(lse.dtype == torch.float32 and lse.shape == shape[:2] and lse.is_contiguous(),
-          "lse must be [num_tokens, num_heads] float32")
+    if query.dtype != key.dtype:
+        raise ValueError("dtype mismatch")
+    if lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
+        raise ValueError("lse must be [num_tokens, num_heads] float32")
     S = _prompt_starts(seq_starts)
     W = _weights_columns(weights, S, Hk)
     dt = _dtype_code(query)
@@ -489,10 +496,11 @@ def pa_decode_weights(out: torch.Tensor, weights: torch.Tensor, workspace, query
     tokens of each context); workspace: a WeightsWorkspace for these sizes."""
     S, H, D, NB, bs, Hk, MB, dt = _attention_common(query, key_cache, value_cache,
                                                     block_tables, context_lens)
-    _need(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
-          "out must match query")
+    if out.shape != query.shape or out.dtype != query.dtype or not out.is_contiguous():
+        raise ValueError("out must match query")
     W = _weights_columns(weights, S, Hk)
-    _need(context_lens.is_contiguous(), "context_lens must be contiguous")
+    if not context_lens.is_contiguous():
+        raise ValueError("context_lens must be contiguous")
     buf = workspace.buffer
     s = _stream_on_one_device(stream, query, out, weights, buf, key_cache, value_cache,
                               block_tables, context_lens)
@@ -514,15 +522,16 @@ def _evict_common(weights, positions, source, new_lens, context_lens, recorded_l
     if (source.dtype != i32 or len(budget) != 3 or budget[0] != S or budget[1] != Hk or
             not source.is_contiguous()):
         raise ValueError("source must be [num_seqs, num_kv_heads, budget] int32")
+    per_seq = (S,)
     for t in (new_lens, context_lens, recorded_lens, seq_lens):
-        if t.dtype != i32 or t.shape != (S,) or not t.is_contiguous():
+        if t.dtype != i32 or t.shape != per_seq or not t.is_contiguous():
             raise ValueError("new_lens, context_lens, recorded_lens and seq_lens must be "
                              "[num_seqs] int32")
-    at = new_lens.data_ptr()
-    if S and (at == context_lens.data_ptr() or at == recorded_lens.data_ptr() or
-              at == seq_lens.data_ptr()):
+    at = (new_lens.data_ptr(), context_lens.data_ptr(), recorded_lens.data_ptr(),
+          seq_lens.data_ptr())
+    if S and at[0] in at[1:]:
         raise ValueError("new_lens must not share storage with the lengths it is found from")
-    return S, Hk, W, budget[2]
+    return S, Hk, W, budget[2], at
 
 
 def pa_evict_select(source: torch.Tensor, new_lens: torch.Tensor, weights: torch.Tensor,
@@ -532,14 +541,13 @@ def pa_evict_select(source: torch.Tensor, new_lens: torch.Tensor, weights: torch
     """Which tokens of every (sequence, KV head) stay: source [S, Hk, budget]
     int32 receives, for each slot of the packed cache, the slot its row comes
     from; new_lens [S] int32 the packed lengths."""
-    S, Hk, W, B = _evict_common(weights, positions, source, new_lens, context_lens,
-                                recorded_lens, seq_lens)
+    S, Hk, W, B, lens = _evict_common(weights, positions, source, new_lens, context_lens,
+                                      recorded_lens, seq_lens)
     s = _stream_on_one_device(stream, weights, positions, source, new_lens, context_lens,
                               recorded_lens, seq_lens)
-    st = load().pa_evict_select(source.data_ptr(), new_lens.data_ptr(), weights.data_ptr(),
-                                positions.data_ptr(), context_lens.data_ptr(),
-                                recorded_lens.data_ptr(), seq_lens.data_ptr(), S, Hk, W, B, int(sink),
-                                int(recent), s)
+    new, ctx, recorded, seq = lens
+    st = load().pa_evict_select(source.data_ptr(), new, weights.data_ptr(), positions.data_ptr(),
+                                ctx, recorded, seq, S, Hk, W, B, int(sink), int(recent), s)
     _check(st, "pa_evict_select")
 
 
@@ -549,25 +557,27 @@ def pa_evict_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, weights
                      recorded_lens: torch.Tensor, seq_lens: torch.Tensor, stream=None) -> None:
     """Move the rows, weights and positions that pa_evict_select kept into the
     first new_lens[s] slots; caches [NB, bs, Hk, D] contiguous, 16-bit or uint8."""
-    S, Hk, W, B = _evict_common(weights, positions, source, new_lens, context_lens,
-                                recorded_lens, seq_lens)
+    S, Hk, W, B, lens = _evict_common(weights, positions, source, new_lens, context_lens,
+                                      recorded_lens, seq_lens)
     shape = key_cache.shape
     NB, bs, Hk2, D = shape
-    _need(Hk2 == Hk, "caches and weights differ in num_kv_heads")
-    _need(value_cache.shape == shape and key_cache.dtype == value_cache.dtype,
-          "key/value caches differ")
-    _need(key_cache.is_contiguous() and value_cache.is_contiguous(), "caches must be contiguous")
-    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and
-          block_tables.shape[0] == S and block_tables.is_contiguous(),
-          "block_tables must be [num_seqs, max_blocks] int32 contiguous")
+    if Hk2 != Hk:
+        raise ValueError("caches and weights differ in num_kv_heads")
+    if value_cache.shape != shape or key_cache.dtype != value_cache.dtype:
+        raise ValueError("key/value caches differ")
+    if not (key_cache.is_contiguous() and value_cache.is_contiguous()):
+        raise ValueError("caches must be contiguous")
+    blocks = block_tables.shape
+    if (block_tables.dtype != torch.int32 or len(blocks) != 2 or blocks[0] != S or
+            not block_tables.is_contiguous()):
+        raise ValueError("block_tables must be [num_seqs, max_blocks] int32 contiguous")
     s = _stream_on_one_device(stream, key_cache, value_cache, weights, positions, source, new_lens,
                               block_tables, context_lens, recorded_lens, seq_lens)
+    new, ctx, recorded, seq = lens
     st = load().pa_evict_compact(key_cache.data_ptr(), value_cache.data_ptr(),
-                                 weights.data_ptr(), positions.data_ptr(), source.data_ptr(),
-                                 new_lens.data_ptr(), block_tables.data_ptr(),
-                                 context_lens.data_ptr(), recorded_lens.data_ptr(),
-                                 seq_lens.data_ptr(), S, Hk, D, NB, bs, block_tables.shape[1], W,
-                                 B, key_cache.element_size(), s)
+                                 weights.data_ptr(), positions.data_ptr(), source.data_ptr(), new,
+                                 block_tables.data_ptr(), ctx, recorded, seq, S, Hk, D, NB, bs,
+                                 blocks[1], W, B, key_cache.element_size(), s)
     _check(st, "pa_evict_compact")
 
 
