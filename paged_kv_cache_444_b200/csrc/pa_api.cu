@@ -1351,6 +1351,8 @@ extern "C" pa_status pa_evict_compact(void* key_cache, void* value_cache, float*
 // <<< eviction
 
 // >>> decode that adds up attention weights (pa_decode_weights): host side.
+#include <algorithm>
+
 #include "pa_decode_weights.cuh"
 
 namespace {
@@ -1369,12 +1371,14 @@ int64_t weights_part(int64_t rows, int64_t cap) {
   return part;
 }
 
-// The offsets hold for every num_kv_heads: for the smallest partitions, those of
-// 16 query heads a KV head.
+// The offsets hold for every num_kv_heads, and a workspace for smaller calls too:
+// partitions below kWeightsPart are fewer than 2 kWeightsCtas for all KV heads, of
+// up to 16 query heads each.
 WeightsLayout weights_layout(int64_t S, int64_t H, int64_t D, int64_t MB, int64_t bs) {
   WeightsLayout l{};
-  const int64_t part = weights_part((S * H + 15) / 16, MB * bs);
-  const int64_t rows = S * H * ((MB * bs + part - 1) / part);
+  auto parts = [&](int64_t part) { return S * H * ((MB * bs + part - 1) / part); };
+  const int64_t few = std::min<int64_t>(16 * 2 * kWeightsCtas, parts(kWeightsPartMin));
+  const int64_t rows = std::max(parts(kWeightsPart), few);
   const int64_t sizes[4] = {rows * D * 4, rows * 4, rows * 4, S * H * MB * bs * 4};
   for (int i = 0; i < 4; ++i) {
     l.off[i] = l.total;

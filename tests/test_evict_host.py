@@ -141,6 +141,23 @@ def test_prompt_weights_refusals(want, kw):
     assert _call("pa_prompt_weights", PW_ORDER, PW_BASE, **kw) == want
 
 
+def test_a_workspace_serves_smaller_calls():
+    """Fewer sequences or narrower tables never need more."""
+    from paged_kv_cache_444_b200._lib import load
+    size = load().pa_decode_weights_workspace_bytes
+    for H, D in ((32, 128), (5, 64), (64, 64)):
+        last = 0
+        for S in range(0, 300):
+            n = size(S, H, D, 40, 16)
+            assert n >= last
+            last = n
+        last = 0
+        for MB in range(1, 700):
+            n = size(7, H, D, MB, 16)
+            assert n >= last
+            last = n
+
+
 def test_eviction_state_refuses_a_budget_that_cannot_hold():
     EvictionState(1, 1, 32, 8, "cpu", sink=3, recent=5)
     for bad in (dict(sink=4, recent=5), dict(sink=9), dict(sink=-1), dict(recent=-1)):

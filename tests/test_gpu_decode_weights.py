@@ -278,3 +278,17 @@ def test_offsets_beyond_32_bits_with_a_cta_a_context(cuda_device):
     b.context_lens[2:1096] = 0        # check the first and the last ones
     out[2:1096], weights[2:1096] = 0, 0
     _check(b, before, weights, out, 1, b.cfg.scale)
+
+
+def test_one_workspace_for_batches_of_many_sizes(cuda_device):
+    """That of the largest batch, whose partitions are the longest ones."""
+    big = _batch(cuda_device, (600,) * 230, 8, 2, 64, "f16", 941)
+    ws = WeightsWorkspace.for_call(big.query, big.key_cache, big.block_tables)
+    for ctx in ((600,) * 230, (600, 590) * 50, (600, 1, 530), (40, 5)):
+        b = _batch(cuda_device, ctx, 8, 2, 64, "f16", 942)
+        weights = torch.zeros((len(ctx), 2, 600), device=cuda_device)
+        before = weights.clone()
+        out = _call(b, weights, ws=ws)
+        torch.cuda.synchronize()
+        pa_check_error()
+        _check(b, before, weights, out, 1, b.cfg.scale)
