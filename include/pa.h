@@ -400,8 +400,9 @@ pa_status pa_prompt_weights(float *weights, const void *query, const void *key,
  *              (1 in a decode step; entries behind the context stay as they are,
  *              so nothing needs clearing.)
  *   workspace  caller-owned device memory, 256-byte aligned, of at least
- *              pa_decode_weights_workspace_bytes(...) bytes; holds nothing
- *              between calls, and calls that may overlap need one each
+ *              pa_decode_weights_workspace_bytes(...) bytes (one of that
+ *              size serves every smaller call too); holds nothing between
+ *              calls, and calls that may overlap need one each
  * Other arguments, layouts and limits as pa_decode.  A context longer than
  * max_tokens is reported (PA_CHECK_CONTEXT_LEN): its output is computed, its
  * weights stay as they were.
