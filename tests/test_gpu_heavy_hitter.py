@@ -202,3 +202,71 @@ def test_state_is_graph_capturable(cuda_device):
             assert np.array_equal(rows, s * 64 + source[s, 0, :n])
             assert np.array_equal(state.positions[s, 0, :n].cpu().numpy(), source[s, 0, :n])
     pa_check_error()
+
+
+class Layer:
+    """One layer's tensors of its own, from a seed: a step from packed prompts to a
+    decode step over the evicted cache."""
+
+    def __init__(self, dev, seed):
+        g = torch.Generator(device=dev).manual_seed(seed)
+        self.lens = ((900, 33, 410), (1700,), (300,) * 7)[seed % 3]
+        self.S, T, self.width = len(self.lens), sum(self.lens), max(self.lens)
+        rand = lambda *s: torch.randn(s, generator=g, device=dev).bfloat16()
+        self.q, self.k, self.v = rand(T, 16, 128), rand(T, 4, 128), rand(T, 4, 128)
+        self.query = rand(self.S, 16, 128)
+        starts = np.concatenate([[0], np.cumsum(self.lens)])
+        blocks = -(-self.width // 16)
+        self.tables = torch.arange(self.S * blocks, dtype=torch.int32, device=dev).view(self.S, -1)
+        slots = np.concatenate([s * blocks * 16 + np.arange(n) for s, n in enumerate(self.lens)])
+        self.slots = torch.as_tensor(slots, device=dev)
+        self.starts = torch.tensor(starts, dtype=torch.int32, device=dev)
+        self.length = torch.tensor(self.lens, dtype=torch.int32, device=dev)
+        self.kc = torch.zeros((self.S * blocks, 16, 4, 128), dtype=torch.bfloat16, device=dev)
+        self.vc = torch.zeros_like(self.kc)
+        self.ctx = self.length.clone()
+        self.state = EvictionState(self.S, 4, self.width, 128, dev, 4, 20)
+        self.ws = WeightsWorkspace.for_call(self.query, self.kc, self.tables)
+        self.out, self.step = torch.zeros_like(self.q), torch.zeros_like(self.query)
+        self.lse = torch.zeros((T, 16), device=dev)
+
+    def run(self):
+        self.ctx.copy_(self.length)
+        self.state.recorded_lens.zero_()
+        prompt_step(self.q, self.k, self.v, self.kc, self.vc, self.slots, self.starts, 0.09,
+                    out=self.out, lse=self.lse, weights=self.state.weights, window=200)
+        self.state.evict(self.kc, self.vc, self.tables, self.ctx, self.length)
+        pa_decode_weights(self.step, self.state.weights, self.ws, self.query, self.kc, self.vc,
+                          self.tables, self.ctx, 0.09, 0)
+
+    def results(self):
+        return [t.clone() for t in (self.out, self.lse, self.step, self.state.weights,
+                                    self.state.positions, self.state.source, self.kc, self.ctx)]
+
+
+def test_layers_at_once_on_streams_and_in_graphs(cuda_device):
+    """Three layers one after another, then at the same time on a stream each, eager and as
+    captured graphs: the same bits."""
+    layers = [Layer(cuda_device, seed) for seed in range(3)]
+    for layer in layers:
+        layer.run()
+    torch.cuda.synchronize()
+    want = [layer.results() for layer in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    graphs = []
+    for layer in layers:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            layer.run()
+    for again in range(6):
+        for layer, stream, graph in zip(layers, streams, graphs):
+            with torch.cuda.stream(stream):
+                if again % 2:
+                    graph.replay()
+                else:
+                    layer.run()
+        torch.cuda.synchronize()
+        pa_check_error()
+        for layer, bits in zip(layers, want):
+            for got, ours in zip(layer.results(), bits):
+                assert torch.equal(got, ours)
