@@ -1290,6 +1290,10 @@ extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const f
     return launch_select<512, 9>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 256 * 18) return launch_select<256, 18>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 512 * 18) return launch_select<512, 18>(a, rows, c, run, shift, as_stream(stream));
+  // few long rows have an SM a CTA (one of 131072 slots: 16.4 us; streamed, 22.1;
+  // but 16 of 110000, whose clusters are not all resident at once so: 29.5 and 22.5)
+  if (run <= 512 * 32 && rows * c * 2 <= sms)
+    return launch_select<512, 32>(a, rows, c, run, shift, as_stream(stream));
   return launch_select<512, 0>(a, rows, c, run, shift, as_stream(stream));
 }
 

@@ -66,9 +66,10 @@ __device__ __forceinline__ long long slot_position(const int32_t* positions, int
 // was built again for each digit and ranked a slot at a time (315 instructions
 // a word).  128 x 8 rows of 1017 slots: 9.2 us; 31 us with 512 threads and three
 // digits of 11 bits, 12.1 us with each word's bounds looked at in every pass.  One
-// row of 131072 slots, eight CTAs: 21.4 us, in cycles about a tenth each for the
-// top digit and its exchange, a fifth for flags and lists, the rest shared between
-// the other digits and the ranks and list.
+// row of 131072 slots, eight CTAs with their keys in registers: 16.4 us; streamed,
+// 22 us, in cycles about a tenth each for the top digit and its exchange, a fifth
+// for flags and lists, the rest shared between the other digits and the ranks and
+// list.
 // ---------------------------------------------------------------------------
 
 // kHeld: words of keys a warp keeps in registers, or 0: it loads them again
@@ -113,13 +114,13 @@ __device__ __forceinline__ void add_cluster_u32(uint32_t addr, uint32_t v) {
 }
 
 template <int kThreadsN, int kHeld>
-__global__ void __launch_bounds__(kThreadsN, 1024 / kThreadsN)
+__global__ void __launch_bounds__(kThreadsN, kHeld > 18 ? 1 : 1024 / kThreadsN)
     evict_select_kernel(const EvictArgs a, int max_run, int list_shift) {
   using L = SelectSmem<kThreadsN, kHeld>;
   constexpr bool kReg = kHeld > 0;
   constexpr int kWarpsN = L::kWarpsN, kBins = L::kBins;
-  constexpr int kBatch = kReg ? 9 : 8;                 // words a warp loads before it uses any
-  static_assert(kHeld % 9 == 0, "words in registers come in whole batches");
+  constexpr int kBatch = kReg && kHeld % 9 == 0 ? 9 : 8;   // words a warp loads before it uses any
+  static_assert(kHeld % kBatch == 0 && kHeld <= 32, "whole batches, a flag word a lane");
   extern __shared__ __align__(16) uint8_t smem[];
   uint2* cand = reinterpret_cast<uint2*>(smem + L::kCand);
   uint32_t* scan = reinterpret_cast<uint32_t*>(smem + L::kScan);

@@ -371,3 +371,27 @@ def _few_numbers(rng, shape):
 def test_select_where_nan_decides(ctx, Hk, budget, recorded, cuda_device):
     b = Batch(cuda_device, ctx, Hk, budget, 99, recorded=recorded, weights=_few_numbers)
     b.check_select(2, 11)
+
+
+@pytest.mark.parametrize("weights", [None, _ties, _odd, _few_numbers],
+                         ids=["random", "ties", "odd", "nan"])
+@pytest.mark.parametrize("n,Hk,B", [(131072, 1, 4096), (100001, 2, 30000)])
+def test_select_of_few_long_rows(n, Hk, B, weights, cuda_device):
+    """Up to 16384 slots a CTA in registers, an SM for each.  A stable sort stands in for the
+    slow loop."""
+    b = Batch(cuda_device, (n,), Hk, B, 90, weights=weights)
+    b.select(4, 50)
+    torch.cuda.synchronize()
+    pa_check_error()
+    for h in range(Hk):
+        w = b.weights[0, h].astype(np.float64)
+        rank = np.where(np.isnan(w), -np.inf, w)
+        lower = np.isnan(w)                       # NaN counts below -inf
+        held = np.zeros(n, bool)
+        held[:4] = held[n - 50:] = True
+        order = np.lexsort((np.arange(n), -rank, lower, ~held))
+        kept = np.zeros(n, bool)
+        kept[order[:B]] = True
+        want = np.arange(B)
+        want[~kept[:B]] = B + np.flatnonzero(kept[B:])
+        assert np.array_equal(b.source[0, h].cpu().numpy(), want)
