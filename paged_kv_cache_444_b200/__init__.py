@@ -8,6 +8,8 @@ The compute lives in ``libpa.so`` (CUDA kernels behind the C ABI of
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from ._lib import (DecodePlan, HostStep, PagedAttentionError, load, pa_check_error, pa_copy_blocks, pa_decode,
@@ -62,6 +64,20 @@ class WeightsWorkspace:
         return cls(S, H, D, block_tables.shape[1], query.device, key_cache.shape[1])
 
 
+def _pool_of(stream, device):
+    """Context whose allocations come from the memory pool of the stream that a
+    call is given (None: the current one).  The caching allocator hands memory
+    freed on a stream to that stream's next tensor at once, so a buffer from the
+    current stream's pool may be in use there while the given stream writes it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)        # 0 and 1: the default stream
+        stream = (torch.cuda.ExternalStream(handle, device) if handle > 1
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
 def decode_step(query, key, value, key_cache, value_cache, slot_mapping, block_tables,
                 context_lens, scale: float, out: torch.Tensor | None = None,
                 partition_size: int = 0, workspace: SplitWorkspace | None = None,
@@ -97,12 +113,18 @@ def prompt_step(query, key, value, key_cache, value_cache, slot_mapping, seq_sta
     rows into the cache (pa_reshape_and_cache; key_cache None: no write), attend
     (pa_prompt_attention) and, when weights [S, Hk, max_tokens] is given, set the
     attention weight each token receives from the last `window` tokens of its
-    prompt, all of them if None (pa_prompt_weights).  All tensors live on one CUDA device."""
+    prompt, all of them if None (pa_prompt_weights).  All tensors live on one CUDA
+    device.  What is allocated here belongs to `stream`; the returned out may be
+    used on the current stream too, once that has waited for `stream`."""
     T, H, _ = query.shape
-    if out is None:
-        out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
-    if weights is not None and lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=query.device)
+    with _pool_of(stream, query.device):
+        made = out is None
+        if made:
+            out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+        if weights is not None and lse is None:
+            lse = torch.empty((T, H), dtype=torch.float32, device=query.device)
+    if made and stream is not None:
+        out.record_stream(torch.cuda.current_stream(query.device))
     if key_cache is not None:
         pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, stream)
     pa_prompt_attention(out, lse, query, key, value, seq_starts, scale, stream)
