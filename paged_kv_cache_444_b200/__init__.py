@@ -84,17 +84,23 @@ def decode_step(query, key, value, key_cache, value_cache, slot_mapping, block_t
                 stream=None) -> torch.Tensor:
     """One decode step of one attention layer: write this step's K/V rows
     (pa_reshape_and_cache), then attend (pa_decode, or pa_decode_split +
-    pa_reduce when partition_size > 0).  All tensors live on one CUDA device."""
+    pa_reduce when partition_size > 0).  All tensors live on one CUDA device.
+    What is allocated here belongs to `stream`; the returned out may be used on
+    the current stream too, once that has waited for `stream`."""
     if out is None:
-        out = torch.empty_like(query)
+        with _pool_of(stream, query.device):
+            out = torch.empty_like(query)
+        if stream is not None:
+            out.record_stream(torch.cuda.current_stream(query.device))
     if key is not None and key.shape[0] > 0:
         pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, stream)
     if partition_size > 0:
         if workspace is None:
             bs = key_cache.shape[1]
             P = (block_tables.shape[1] * bs + partition_size - 1) // partition_size
-            workspace = SplitWorkspace(query.shape[0], query.shape[1], query.shape[2], P,
-                                       query.device)
+            with _pool_of(stream, query.device):
+                workspace = SplitWorkspace(query.shape[0], query.shape[1], query.shape[2], P,
+                                           query.device)
         pa_decode_split(workspace.tmp_out, workspace.max_logits, workspace.exp_sums, query,
                         key_cache, value_cache, block_tables, context_lens, scale,
                         partition_size, stream)
@@ -117,14 +123,14 @@ def prompt_step(query, key, value, key_cache, value_cache, slot_mapping, seq_sta
     device.  What is allocated here belongs to `stream`; the returned out may be
     used on the current stream too, once that has waited for `stream`."""
     T, H, _ = query.shape
-    with _pool_of(stream, query.device):
-        made = out is None
-        if made:
+    if out is None:
+        with _pool_of(stream, query.device):
             out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
-        if weights is not None and lse is None:
+        if stream is not None:
+            out.record_stream(torch.cuda.current_stream(query.device))
+    if weights is not None and lse is None:
+        with _pool_of(stream, query.device):
             lse = torch.empty((T, H), dtype=torch.float32, device=query.device)
-    if made and stream is not None:
-        out.record_stream(torch.cuda.current_stream(query.device))
     if key_cache is not None:
         pa_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, stream)
     pa_prompt_attention(out, lse, query, key, value, seq_starts, scale, stream)

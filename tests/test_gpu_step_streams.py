@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_444_b200 as pa
+from paged_kv_cache_444_b200 import workloads
 
 pytestmark = pytest.mark.gpu
 BUSY = 50_000_000            # cycles of a spinning kernel, some 25 ms
@@ -74,3 +75,36 @@ def test_prompt_step_on_the_default_stream_by_handle(cuda_device):
     assert torch.equal(pa.prompt_step(**a, stream=0), want)
     torch.cuda.synchronize()
     pa.pa_check_error()
+
+
+@pytest.mark.parametrize("kind", ["torch", "handle"])
+def test_decode_step_owns_what_it_allocates(kind, cuda_device, monkeypatch):
+    """The same for decode_step: its output, and the workspace of the split form."""
+    cfg = workloads.CONFIGS["tiny"]
+    b = workloads.make_batch(cfg, cuda_device)
+    a = (b.query, b.key, b.value, b.key_cache, b.value_cache, b.slot_mapping, b.block_tables,
+         b.context_lens, cfg.scale)
+    want = pa.decode_step(*a, partition_size=16)
+    tmp, real = [], pa.pa_decode_split
+
+    def spy(tmp_out, *rest):
+        tmp.append(tmp_out)
+        return real(tmp_out, *rest)
+
+    monkeypatch.setattr(pa, "pa_decode_split", spy)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    used = torch.empty_like(want)
+    used.fill_(3)
+    used_at = used.data_ptr()
+    del used
+    _busy(side)
+    out = pa.decode_step(*a, partition_size=16, stream=_handles(side)[kind])
+    assert out.data_ptr() != used_at
+    shape, dtype, tmp_at = tmp[0].shape, tmp[0].dtype, tmp.pop().data_ptr()
+    later = [torch.full(shape, 1e30, dtype=dtype, device=cuda_device) for _ in range(4)]
+    assert tmp_at not in [t.data_ptr() for t in later]
+    torch.cuda.synchronize()
+    pa.pa_check_error()
+    assert torch.equal(out, want)
