@@ -468,7 +468,8 @@ pa_status pa_evict_select(int32_t *source, int32_t *new_lens, const float *weigh
  * (pa_copy_blocks).  context_lens, recorded_lens and seq_lens as given to
  * pa_evict_select; new_lens and source must not be written meanwhile.  Repeating
  * the call changes nothing.  A source out of range (PA_CHECK_SOURCE) or a block id
- * out of range (PA_CHECK_BLOCK_ID) is reported and its move left out; a
+ * out of range (PA_CHECK_BLOCK_ID) is reported and its move left out: the slot
+ * keeps its own K and V rows, weight and position (which is recorded); a
  * sequence whose new_lens[s] is no length of its context is reported
  * (PA_CHECK_CONTEXT_LEN) and left as it was.
  */

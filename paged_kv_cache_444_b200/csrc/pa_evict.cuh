@@ -625,20 +625,31 @@ __global__ void __launch_bounds__(kCompactThreads)
   __syncthreads();                                // the count is clear
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int i = i0 + u * kCompactThreads, j = from[u];
+    const int i = i0 + u * kCompactThreads;
+    int j = from[u];
     if (i >= kept) continue;
     if (j != i && (j < kept || j >= n)) {
       record_error(kErrSource, static_cast<long long>(row) * a.e.budget + i);
-      continue;
+      j = i;
     }
-    if (j != i || i >= recorded)
-      a.e.positions[base + i] = static_cast<int32_t>(
-          slot_position(a.e.positions + base, recorded, len, n, j));
-    if (j != i) {
-      a.e.weights[base + i] = a.e.weights[base + j];
+    bool move = j != i;
+    if (move) {
+      // (loaded beside the block ids, not after them)
+      const float weight = a.e.weights[base + j];
+      const int position =
+          static_cast<int>(slot_position(a.e.positions + base, recorded, len, n, j));
       const int src = flat(j), dst = flat(i);
-      if (src >= 0 && dst >= 0) list[atomicAdd(&moves, 1)] = make_int2(src, dst);
+      move = src >= 0 && dst >= 0;
+      if (move) {
+        list[atomicAdd(&moves, 1)] = make_int2(src, dst);
+        a.e.weights[base + i] = weight;
+        a.e.positions[base + i] = position;
+      }
     }
+    // a token that stays, or whose move is left out, keeps its own position
+    if (!move && i >= recorded)
+      a.e.positions[base + i] =
+          static_cast<int>(slot_position(a.e.positions + base, recorded, len, n, i));
   }
   __syncthreads();
   const int units = moves * a.row_units;

@@ -395,3 +395,34 @@ def test_select_of_few_long_rows(n, Hk, B, weights, cuda_device):
         want = np.arange(B)
         want[~kept[:B]] = B + np.flatnonzero(kept[B:])
         assert np.array_equal(b.source[0, h].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("block", [None, 2, 1], ids=["source", "from", "to"])
+def test_compact_leaves_a_slot_whole_where_its_move_is_left_out(block, cuda_device):
+    """A move that is left out, for its source or for the block id at either end, leaves
+    the slot's weight and position beside its own K and V rows; the position is recorded."""
+    b = Batch(cuda_device, (40, 40, 40), 2, 20, 87, recorded=(0, 17, 30))
+    kc, vc, tables, kd, vd = _caches(cuda_device, b, 64, torch.float16, 16, 88)
+    source = np.broadcast_to(np.arange(20, dtype=np.int32), (3, 2, 20)).copy()
+    source[:, :, 14:] = np.arange(34, 40)              # slots 14, 15 and 16 .. 19
+    new, stay = np.full(3, 20, dtype=np.int32), source.copy()
+    given, broken = source.copy(), tables.copy()
+    for s in range(3):
+        if block is None:
+            given[s, 1, 18] = (40, 3, -1)[s]
+            stay[s, 1, 18] = 18
+        else:
+            broken[s, block] = (-1, len(kc), 1 << 30)[s]
+            at = slice(14, 20) if block == 2 else slice(16, 20)
+            stay[s, :, at] = np.arange(20)[at]
+    want = ref.compact(kc, vc, b.weights, b.positions, stay, new, tables, b.ctx, b.recorded,
+                       b.length)
+    w, p = b.t["weights"], b.t["positions"]
+    for again in range(2):
+        pa_evict_compact(kd, vd, w, p, _i32(given, cuda_device), _i32(new, cuda_device),
+                         _i32(broken, cuda_device), b.t["ctx"], b.t["recorded"], b.t["length"])
+        with pytest.raises(PagedAttentionError, match="source" if block is None else "block_id"):
+            pa_check_error()
+        assert np.array_equal(_bits(kd), want[0]) and np.array_equal(_bits(vd), want[1])
+        assert np.array_equal(w.cpu().numpy(), want[2])
+        assert np.array_equal(p.cpu().numpy(), want[3])
