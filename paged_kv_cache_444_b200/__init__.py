@@ -160,17 +160,22 @@ class EvictionState:
         self.recorded_lens = torch.zeros(num_seqs, **i32)
         self.source = torch.empty(rows + (budget,), **i32)
         self.new_lens = torch.empty(num_seqs, **i32)
+        self._unusable = torch.empty(num_seqs, dtype=torch.bool, device=device)
 
     def evict(self, key_cache, value_cache, block_tables, context_lens, seq_lens) -> None:
         """Evict down to the budget on the current stream: select, move the kept
         rows to the front, and set context_lens to the new lengths.  seq_lens [S]
         int32 counts the tokens each sequence has had in all (it must not share
-        storage with context_lens).  Capturable in a CUDA graph."""
+        storage with context_lens).  A length outside [0, max_tokens] is reported
+        (pa_check_error) and stays, with all of its sequence.  Capturable in a
+        CUDA graph."""
         if seq_lens.data_ptr() == context_lens.data_ptr() and context_lens.numel():
             raise ValueError("seq_lens must not share storage with context_lens")
         pa_evict_select(self.source, self.new_lens, self.weights, self.positions, context_lens,
                         self.recorded_lens, seq_lens, self.sink, self.recent)
         pa_evict_compact(key_cache, value_cache, self.weights, self.positions, self.source,
                          self.new_lens, block_tables, context_lens, self.recorded_lens, seq_lens)
-        context_lens.copy_(self.new_lens)
-        self.recorded_lens.copy_(self.new_lens)
+        # a new length of 0 is that of an empty sequence, or of a length that cannot be
+        torch.eq(self.new_lens, 0, out=self._unusable).logical_and_(context_lens)
+        for lens in (context_lens, self.recorded_lens):
+            torch.where(self._unusable, lens, self.new_lens, out=lens)

@@ -8,8 +8,9 @@ import pytest
 import torch
 
 import evict_reference as ref
-from paged_kv_cache_444_b200 import (EvictionState, WeightsWorkspace, pa_check_error,
-                                     pa_decode_weights, pa_reshape_and_cache, prompt_step)
+from paged_kv_cache_444_b200 import (EvictionState, PagedAttentionError, WeightsWorkspace,
+                                     pa_check_error, pa_decode_weights, pa_reshape_and_cache,
+                                     prompt_step)
 from weights_reference import HALF, attend, out_bound
 
 pytestmark = pytest.mark.gpu
@@ -270,3 +271,39 @@ def test_layers_at_once_on_streams_and_in_graphs(cuda_device):
         for layer, bits in zip(layers, want):
             for got, ours in zip(layer.results(), bits):
                 assert torch.equal(got, ours)
+
+
+def test_evict_keeps_a_length_it_cannot_use(cuda_device):
+    """A context past the state's columns, or below zero, is reported; its length and what is
+    recorded of it stay, so that the sequence is evicted from once the length is right."""
+    S, W, B = 4, 60, 20
+    state = EvictionState(S, 2, W, B, cuda_device, 1, 3)
+    g = torch.Generator(device=cuda_device).manual_seed(12)
+    state.weights.copy_(torch.rand(state.weights.shape, generator=g, device=cuda_device))
+    kc = torch.randn((S * 4, 16, 2, 64), generator=g, device=cuda_device).half()
+    vc = kc * 2
+    tables = torch.arange(S * 4, dtype=torch.int32, device=cuda_device).view(S, 4)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda_device)
+    ctx, length = i32(60, 61, -2, 0), i32(60, 70, 30, 0)
+    state.recorded_lens.copy_(i32(0, 7, 5, 7))
+    state.positions[1:, :, :7] = 3 * torch.arange(7, dtype=torch.int32, device=cuda_device)
+    kept = [t[1:3].clone() for t in (state.weights, state.positions)]
+    rows = kc[4:12].clone()
+    state.evict(kc, vc, tables, ctx, length)
+    with pytest.raises(PagedAttentionError, match="context_len, index [12]"):
+        pa_check_error()
+    assert ctx.tolist() == [20, 61, -2, 0]
+    assert state.recorded_lens.tolist() == [20, 7, 5, 0]
+    for was, t in zip(kept, (state.weights, state.positions)):
+        assert torch.equal(was, t[1:3])
+    assert torch.equal(rows, kc[4:12])
+    ctx.copy_(i32(20, 50, 20, 0))             # sequence 1: 10 of the tokens dropped by the user
+    length.copy_(i32(60, 59, 30, 0))
+    recorded = state.recorded_lens.cpu().numpy()
+    source, new = ref.select(state.weights.cpu().numpy(), state.positions.cpu().numpy(), recorded,
+                             length.cpu().numpy(), ctx.cpu().numpy(), B, 1, 3)
+    state.evict(kc, vc, tables, ctx, length)
+    torch.cuda.synchronize()
+    pa_check_error()
+    assert np.array_equal(state.source.cpu().numpy(), source)
+    assert ctx.tolist() == new.tolist() == state.recorded_lens.tolist()
