@@ -17,7 +17,10 @@
 // only when a row outgrows it by 2^8), l the fp32 sum of the fp32 p.  P is
 // rounded to the inputs' type because the product takes both operands in one
 // type: at most 2^-8 (bf16) or 2^-11 (fp16) of each term, as much as the
-// output's own rounding, with random signs over the keys.
+// output's own rounding, with random signs over the keys.  An fp16 P is held 2^7
+// up (2^15 at most, with the slack of m; O and l scale alike): so it is normal down
+// to 2^-21 of m's term and what it loses below is at most 2^-32 of it a key, where
+// thousands of keys at 2^-25 of a large one would have come to nothing.
 //
 // The grid is persistent, one CTA per SM, items longest first, every ring and
 // phase running on from item to item.  Warps: 0-3 and 4-7 the softmax of tiles
@@ -53,6 +56,11 @@ constexpr int kWarpGuard = 10;
 constexpr int kGuardWarps = 2;
 // 384 threads launched at 168 registers: 504 x 128; two warpgroups at 208 and one at 88
 constexpr uint32_t kPromptRegsSoftmax = 208, kPromptRegsOther = 88;
+// log2 of what P is held up by (and with it O and l), and the way back
+template <bool BF16>
+constexpr float kPromptLift = BF16 ? 0.f : 7.f;
+template <bool BF16>
+constexpr float kPromptDrop = BF16 ? 1.f : 0x1p-7f;
 constexpr int kPromptRankSeqs = 256;    // batches ranked longest-first: sequences,
 constexpr int kPromptRankUnits = 2048;  // units (sequence, tile pair),
 constexpr int kPromptRankWork = 65536;  // and units x sequences counted
@@ -366,7 +374,8 @@ __device__ __forceinline__ void prompt_softmax_block(float (&p)[kPrefillKeys], b
   }
   l *= alpha;
   const float ref = m == -INFINITY ? 0.f : m;
-  const float2 neg = make_float2(-ref, -ref), mul2 = make_float2(mul, mul);
+  const float up = kPromptLift<BF16> - ref;
+  const float2 neg = make_float2(up, up), mul2 = make_float2(mul, mul);
   const float2 one = make_float2(1.f, 1.f);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -799,7 +808,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const bool marked = *mark != 0;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // a NaN stays one
       const size_t hrow = static_cast<size_t>(it.q0 + tok) * a.num_heads + it.kvh * G + row % G;
-      if (live && a.lse && (!kHalves || t == 0)) a.lse[hrow] = m * kLn2 + logf(l);
+      if (live && a.lse && (!kHalves || t == 0))
+        a.lse[hrow] = m * kLn2 + logf(l * kPromptDrop<BF16>);
       // 32 columns at a time through shared memory (16-byte chunk c of row r at
       // c ^ (r / 2 % 4), free of bank conflicts), so that four lanes store a row's
       // 64 bytes: a lane a row touched 32 lines a store, and the epilogue took

@@ -287,3 +287,33 @@ def test_a_single_kv_head_may_have_any_head_stride(cuda_device):
     p.k = wide.as_strided((100, 1, 64), (192, 8, 1), 64)      # one head: its stride says nothing
     p.run().check()
     assert torch.equal(p.out, want)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H,D", [(2, 64), (16, 64), (2, 128), (16, 128)])
+def test_small_weights_beside_a_large_one(H, D, dtype, cuda_device):
+    """One key takes nearly all of the weight and has no value; thousands of keys at 2^-25.7 to
+    2^-26.4 of it make the output.  An fp16 P is below its normal numbers there: an error of
+    2^-25 each, against a sum of at least 2^7 (P is held 2^7 up), is 2^-32 of a value."""
+    n = 5000
+    p = Prompt(cuda_device, (n,), H, H, D, dtype, 94)
+    p.q.zero_()
+    p.q[..., 0] = 8
+    p.k.zero_()
+    step = torch.arange(n, device=cuda_device)
+    p.k[:, :, 0] = (-9.8125 - 0.25 * (step % 3))[:, None].to(p.k.dtype)
+    p.k[0, :, 0] = 8
+    p.v.copy_((500 + 500 * torch.rand(p.v.shape, device=cuda_device)).to(p.v.dtype))
+    p.v[0] = 0
+    p.run(0.125)
+    torch.cuda.synchronize()
+    pa_check_error()
+    half, rows = HALF[p.out.dtype], 300
+    for h in (0, H - 1):
+        _, o, lse, rel, pv = attend(p.q[n - rows:, h], p.k[:, h], p.v[:, h], 0.125, n - rows)
+        lim = (half * o.abs() + (half + 2 * rel[:, None] + n * 2.0 ** -23) * pv +
+               (n * 2.0 ** -32 * 1000 + 2.0 ** -25) * (dtype == "f16")) * (1 + half)
+        err = (p.out[n - rows:, h].double() - o).abs()
+        assert (err <= lim).all(), (h, float((err / lim).max()))
+        err = (p.lse[n - rows:, h].double() - lse).abs()
+        assert (err <= rel + 2.0 ** -21 + 2.0 ** -23 * lse.abs() + n * 2.0 ** -23).all()
