@@ -86,12 +86,17 @@ __device__ __forceinline__ void tma_load_4d_once(uint32_t dst, const CUtensorMap
 // Per-warp state and page step: S^T = K Q^T, O^T = V^T P^T for NT tiles of 8
 // query heads, the logits of the page's tokens written to z.  bf16 P goes in
 // as a hi + lo pair; the reference max may trail the true one by 2^kSlack.
+// fp16 P is one operand, as in pa_decode (at most 2^-11 of each term, the
+// output's own rounding; a pair's lo of 0 would make NaN of an infinite value),
+// held 2^kLift up until publish: 2^15 at most, normal down to 2^-21 of the
+// reference, off by at most 2^-32 of it a token below.
 // ---------------------------------------------------------------------------
 template <int D, bool BF16, int NT>
 struct WeightsWarp {
   static constexpr int KSTEPS = D / 16;
   static constexpr int MTILES = D / 16;
   static constexpr float kSlack = 8.f;
+  static constexpr float kLift = BF16 ? 0.f : 7.f, kDrop = BF16 ? 1.f : 0x1p-7f;
   uint32_t qb[KSTEPS][NT][2];   // Q^T B fragments of query row 8 n + lane / 4
   float acc[MTILES][NT][4];     // O^T: (dim 16c + g, rows 8n + 2t, + 1), (dim 16c + 8 + g, ...)
   float m[NT][2], l[NT][2], mt[NT][2];
@@ -190,8 +195,8 @@ struct WeightsWarp {
     uint32_t pb[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-      const float r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+      const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kLift;
+      const float r1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kLift;
       const float p0 = ex2(x[n][0] - r0), p1 = ex2(x[n][1] - r1);
       const float p2 = ex2(x[n][2] - r0), p3 = ex2(x[n][3] - r1);
       const uint32_t h_lo = pack2<BF16>(p0, p1), h_hi = pack2<BF16>(p2, p3);
@@ -228,7 +233,7 @@ struct WeightsWarp {
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float f = mt[n][h] > -INFINITY ? ex2(m[n][h] - mt[n][h]) : 1.f;
+        const float f = kDrop * (mt[n][h] > -INFINITY ? ex2(m[n][h] - mt[n][h]) : 1.f);
         float lh = l[n][h] * f;
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) lh += __shfl_xor_sync(0xffffffffu, lh, o);

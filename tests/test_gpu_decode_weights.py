@@ -8,7 +8,7 @@ import torch
 from paged_kv_cache_444_b200 import (PagedAttentionError, WeightsWorkspace, pa_check_error,
                                      pa_decode, pa_decode_weights, workloads)
 from parity_helpers import grow_logits, poison_past_context
-from weights_reference import attend, out_bound
+from weights_reference import HALF, attend, out_bound
 
 pytestmark = pytest.mark.gpu
 BASE = workloads.CONFIGS["gqa_llama3_8b"]
@@ -292,3 +292,39 @@ def test_one_workspace_for_batches_of_many_sizes(cuda_device):
         torch.cuda.synchronize()
         pa_check_error()
         _check(b, before, weights, out, 1, b.cfg.scale)
+
+
+@pytest.mark.parametrize("n,heads,kv_heads", [(500, 4, 2), (500, 12, 1), (3000, 8, 2), (3000, 9, 1)],
+                         ids=["one_cta", "one_cta_wide", "split", "split_wide"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_small_weights_beside_a_large_one(dtype, n, heads, kv_heads, cuda_device):
+    """One key takes nearly all of the weight and has no value; the others, at 2^-25.7 to
+    2^-26.4 of it, make the output.  Where a warp has both, its fp16 P is below its normal
+    numbers: an error of 2^-25 each, against a sum of at least 2^7 (P is held 2^7 up), is 2^-32
+    of a value.  It has at most a quarter of 512 tokens."""
+    b = _batch(cuda_device, (n, 33), heads, kv_heads, 64, dtype, 943)
+    b.query.zero_()
+    b.query[..., 0] = 8
+    b.key_cache.zero_()
+    own = b.block_tables[0, :-(-n // 16)].long()
+    step = torch.arange(own.numel() * 16, device=cuda_device).view(-1, 16, 1)
+    b.key_cache[own, :, :, 0] = (-9.8125 - 0.25 * (step % 3)).to(b.key_cache.dtype).expand(
+        -1, -1, kv_heads)
+    b.key_cache[own[0], 0, :, 0] = 8
+    b.value_cache.copy_(500 + 500 * torch.rand(b.value_cache.shape, device=cuda_device))
+    b.value_cache[own[0], 0] = 0
+    weights = torch.zeros((2, kv_heads, n), device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights, scale=0.125)
+    torch.cuda.synchronize()
+    pa_check_error()
+    _check(b, before, weights, out, 1, 0.125)
+    at, G = torch.arange(n, device=cuda_device), heads // kv_heads
+    for kv in range(kv_heads):
+        k, v = (c[own[at // 16], at % 16, kv] for c in (b.key_cache, b.value_cache))
+        _, o, _, rel, pv = attend(b.query[0, kv * G:(kv + 1) * G], k, v, 0.125)
+        half, p_half = HALF[out.dtype], 2.0 ** -16 if dtype == "bf16" else 2.0 ** -11
+        lim = (half * o.abs() + (p_half + 2 * rel[:, None] + n * 2.0 ** -23) * pv +
+               (128 * 2.0 ** -32 * 1000 + 2.0 ** -25) * (dtype == "f16")) * (1 + half)
+        err = (out[0, kv * G:(kv + 1) * G].double() - o).abs()
+        assert (err <= lim).all(), (kv, float((err / lim).max()))
