@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
           const float4* lse4 = reinterpret_cast<const float4*>(lse_sh + sl * 128);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           if (rows == q_rows && tok0 >= kb + 127) {
-            // every column counts (those past q_rows have an lse of +inf)
+            // every column counts (those past q_rows are 0 and have an lse of +inf)
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               float u[32];
@@ -411,6 +411,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
               if (c == 3) {
                 tmem_fence_before_sync();
                 mbar_arrive(empty);                    // S is in registers
+                if (q_rows < 128) {
+                  // (a zero query row times an infinite key is NaN; at least 117 rows are live)
+#pragma unroll
+                  for (int e = 117 - 96; e < 32; ++e) u[e] = 96 + e < q_rows ? u[e] : 0.f;
+                }
               }
               add_columns(u, lse4 + 8 * c, scale, sum);
             }

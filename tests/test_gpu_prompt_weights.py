@@ -203,3 +203,25 @@ def test_offsets_beyond_32_bits(cuda_device):
     p = Prompt(cuda_device, tuple(range(1, 41)), 8, 8, 64, "f16", 79)
     weights, lse = _run(p, 100, extra=7_000_000 - 40)
     _check(p, weights, lse, 100, seqs=[0, 38, 39])
+
+
+@pytest.mark.parametrize("H,Hk", [(6, 2), (5, 1), (13, 1), (8, 2)])
+def test_a_key_with_logits_of_minus_infinity_gets_no_weight(H, Hk, cuda_device):
+    """exp(-inf - lse) is 0 for it in full tiles too, whose last columns hold no query row
+    where the group does not divide 128."""
+    p = Prompt(cuda_device, (400, 333), H, Hk, 64, "bf16", 80)
+    p.q[:, :, 0] = 1 + p.q[:, :, 0].abs()
+    p.k[[7, 150, 407]] = 0
+    p.k[[7, 150, 407], :, 0] = -torch.inf
+    weights, lse = _run(p, 1000)
+    torch.cuda.synchronize()
+    pa_check_error()
+    assert lse.isfinite()[8:400].all() and lse.isfinite()[408:].all()
+    gone = [(0, 7), (0, 150), (1, 7)]
+    for s, j in gone:
+        assert (weights[s, :, j] == 0).all(), (s, j, weights[s, :, j])
+    # the others are what they are when those keys are as far as 16 bits go
+    p.k[[7, 150, 407], :, 0] = -3e38
+    far, far_lse = _run(p, 1000)
+    torch.cuda.synchronize()
+    assert torch.equal(far_lse, lse) and torch.equal(far, weights)
