@@ -147,25 +147,29 @@ __device__ __forceinline__ int warp_uniform(int x) { return __shfl_sync(0xffffff
 // special-function unit (16 results a cycle and SM) would bound: with n the
 // nearest integer of x, s = 2^n and p a polynomial of degree 5 for 2^(x - n),
 // the minimax fit of the relative error on [-1/2, 1/2] (7.5e-8, 2.1e-7 in fp32).
-// Below -126.5 s is 0 (2^-127 has no exponent field), so a masked key's p is; a
-// NaN stays one, +inf gives NaN.
+// The smallest exponents give an s of 0 (no exponent field), so a masked key's p is; a
+// NaN stays one, +inf gives NaN.  kUp: a factor 2^kUp is in p, not in s, so that s
+// has a field up to n = 127 + kUp; the smallest are then those below kUp - 126.5.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+template <int kUp = 0>
 __device__ __forceinline__ void exp2_fma(float2 x, float2& p, float2& s) {
+  constexpr float kTimes = static_cast<float>(1 << kUp);
   auto both = [](float v) { return make_float2(v, v); };
-  x = make_float2(max_nan(x.x, -127.f), max_nan(x.y, -127.f));
+  x = make_float2(max_nan(x.x, kUp - 127.f), max_nan(x.y, kUp - 127.f));
   const float2 t = ffma2(x, both(1.f), both(12582912.f));          // 1.5 * 2^23 + n
   const float2 f = ffma2(ffma2(t, both(1.f), both(-12582912.f)), both(-1.f), x);
-  p = ffma2(f, both(0.0013276472454890609f), both(0.009675540961325169f));
-  p = ffma2(p, f, both(0.05550713092088699f));
-  p = ffma2(p, f, both(0.24022120237350464f));
-  p = ffma2(p, f, both(0.6931469440460205f));
-  p = ffma2(p, f, both(1.0000001192092896f));
-  s = make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
-                  __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u));
+  p = ffma2(f, both(kTimes * 0.0013276472454890609f), both(kTimes * 0.009675540961325169f));
+  p = ffma2(p, f, both(kTimes * 0.05550713092088699f));
+  p = ffma2(p, f, both(kTimes * 0.24022120237350464f));
+  p = ffma2(p, f, both(kTimes * 0.6931469440460205f));
+  p = ffma2(p, f, both(kTimes * 1.0000001192092896f));
+  constexpr uint32_t kBias = static_cast<uint32_t>(127 - kUp) << 23;
+  s = make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + kBias),
+                  __uint_as_float((__float_as_uint(t.y) << 23) + kBias));
 }
 
 // Store 32 32-bit columns of this thread's lane (complete after tmem_wait_st).

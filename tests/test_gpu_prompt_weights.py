@@ -225,3 +225,36 @@ def test_a_key_with_logits_of_minus_infinity_gets_no_weight(H, Hk, cuda_device):
     far, far_lse = _run(p, 1000)
     torch.cuda.synchronize()
     assert torch.equal(far_lse, lse) and torch.equal(far, weights)
+
+
+@pytest.mark.parametrize("down", [60.0, 91.0, 100.0, 250.0])
+def test_weights_beyond_the_largest_number_are_infinite(down, cuda_device):
+    """An lse that is not the attention's own: terms up to exp(down) and past 2^128, where a
+    sum is +inf, as the formula's is in 32 bits; never a finite number that is not it."""
+    p = Prompt(cuda_device, (400, 70), 8, 2, 128, "bf16", 78)
+    lse, scale = _lse(p, 1.0)            # few terms a key are near the largest
+    low = lse - down
+    weights = torch.full((2, 2, 400), 7.0, device=cuda_device)
+    pa_prompt_weights(weights, p.q, p.k, low, p.starts, scale, 400)
+    torch.cuda.synchronize()
+    pa_check_error()
+    top, seen = float(torch.finfo(torch.float32).max), 0
+    for s, (b, n) in enumerate(((0, 400), (400, 70))):
+        later = torch.ones((n, n), dtype=torch.bool, device=cuda_device).triu(1)
+        for kv in range(2):
+            k = p.k[b:b + n, kv].double()
+            want, lim = torch.zeros(n, device=cuda_device).double(), 0.0
+            for h in range(4 * kv, 4 * kv + 4):
+                q = p.q[b:b + n, h].double()
+                z = (q @ k.T * scale).masked_fill(later, -torch.inf)
+                size = (q.abs() @ k.abs().T * scale).masked_fill(later, 0)
+                x = (z - low[b:b + n, h, None].double()).exp()
+                rel = (p.D * 2.0 ** -23 * size + 4 * 2.0 ** -24 * (z.abs().masked_fill(later, 0) +
+                       low[b:b + n, h, None].abs()) + 2.0 ** -21 + (40 + 4 * n // 100) * 2.0 ** -24)
+                want, lim = want + x.sum(0), lim + (x * rel).sum(0)
+            got = weights[s, kv, :n].double()
+            assert (got[want > top + lim] == torch.inf).all()
+            fits = want < top - lim
+            assert ((got - want).abs()[fits] <= lim[fits]).all()
+            seen += int((want > top + lim).sum())
+    assert (seen > 0) == (down > 80)
