@@ -169,7 +169,8 @@ class EvictionState:
         storage with context_lens).  A length outside [0, max_tokens] is reported
         (pa_check_error) and stays, with all of its sequence.  Capturable in a
         CUDA graph."""
-        if seq_lens.data_ptr() == context_lens.data_ptr() and context_lens.numel():
+        apart = abs(seq_lens.data_ptr() - context_lens.data_ptr())
+        if apart < context_lens.element_size() * context_lens.numel():
             raise ValueError("seq_lens must not share storage with context_lens")
         pa_evict_select(self.source, self.new_lens, self.weights, self.positions, context_lens,
                         self.recorded_lens, seq_lens, self.sink, self.recent)

@@ -529,7 +529,8 @@ def _evict_common(weights, positions, source, new_lens, context_lens, recorded_l
                              "[num_seqs] int32")
     at = (new_lens.data_ptr(), context_lens.data_ptr(), recorded_lens.data_ptr(),
           seq_lens.data_ptr())
-    if S and at[0] in at[1:]:
+    new, ctx, recorded, seq = at
+    if S and (abs(new - ctx) < 4 * S or abs(new - recorded) < 4 * S or abs(new - seq) < 4 * S):
         raise ValueError("new_lens must not share storage with the lengths it is found from")
     return S, Hk, W, budget[2], at
 

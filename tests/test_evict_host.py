@@ -172,3 +172,35 @@ def test_eviction_state_refuses_lengths_in_one_tensor():
     lens = torch.full((2,), 20, dtype=torch.int32)
     with pytest.raises(ValueError, match="seq_lens must not share"):
         state.evict(kc, kc.clone(), torch.zeros(2, 2, dtype=torch.int32), lens, lens)
+
+
+@pytest.mark.parametrize("apart", [-3, -1, 0, 1, 3])
+def test_lengths_may_not_overlap_in_part(apart):
+    """Views into one buffer a few entries apart: written in place, the same as one tensor."""
+    buf = torch.zeros(12, dtype=torch.int32)
+    one, other = buf[4:8], buf[4 + apart:8 + apart]
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    good = dict(source=i32(4, 1, 8), new_lens=one, weights=torch.zeros(4, 1, 20),
+                positions=i32(4, 1, 20), context_lens=i32(4), recorded_lens=i32(4),
+                seq_lens=i32(4))
+    for name in ("context_lens", "recorded_lens", "seq_lens"):
+        with pytest.raises(ValueError, match="new_lens must not share"):
+            pa_evict_select(**{**good, name: other}, sink=1, recent=2)
+    state = EvictionState(4, 1, 32, 8, "cpu")
+    kc = torch.zeros(4, 16, 1, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="seq_lens must not share"):
+        state.evict(kc, kc.clone(), i32(4, 2), one, other)
+
+
+def test_lengths_side_by_side_are_apart():
+    """Views that touch without a common entry go on to the next check (host tensors)."""
+    buf = torch.zeros(16, dtype=torch.int32)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        pa_evict_select(source=i32(4, 1, 8), new_lens=buf[4:8], weights=torch.zeros(4, 1, 20),
+                        positions=i32(4, 1, 20), context_lens=buf[:4], recorded_lens=buf[8:12],
+                        seq_lens=buf[12:], sink=1, recent=2)
+    state = EvictionState(4, 1, 32, 8, "cpu")
+    kc = torch.zeros(4, 16, 1, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        state.evict(kc, kc.clone(), i32(4, 2), buf[:4], buf[4:8])
