@@ -328,3 +328,44 @@ def test_small_weights_beside_a_large_one(dtype, n, heads, kv_heads, cuda_device
                (128 * 2.0 ** -32 * 1000 + 2.0 ** -25) * (dtype == "f16")) * (1 + half)
         err = (out[0, kv * G:(kv + 1) * G].double() - o).abs()
         assert (err <= lim).all(), (kv, float((err / lim).max()))
+
+
+def _split_form(rows, cap, group):
+    """Tokens of a partition and of a second-pass CTA, as the launch picks them for `rows`
+    (sequence, KV head) pairs and tables of `cap` tokens (444: three CTAs an SM)."""
+    part, run = 512, 4096
+    while part > 128 and rows * -(-cap // part) < 444:
+        part //= 2
+    while run > 256 and (run * group > 16384 or rows * -(-cap // run) < 444):
+        run //= 2
+    return part, run
+
+
+SPLITS = {
+    # name: (contexts, heads, KV heads, head_dim, partition, run)
+    "parts_512": ((511, 512, 513, 1023, 1024, 1025) + (5,) * 24, 32, 8, 128, 512, 1024),
+    "parts_512_mha": ((512, 1025, 513, 1, 0, 1024) + (3,) * 14, 16, 16, 128, 512, 1024),
+    "parts_512_group16_d64": ((511, 512, 513, 1025) + (7,) * 226, 16, 1, 64, 512, 1024),
+    "runs_4096": ((4095, 4096, 4097, 8192, 8193, 28672, 512, 1), 32, 8, 128, 512, 4096),
+    "runs_2048_group8": ((2047, 2048, 2049, 4096, 28001, 513, 0, 1), 64, 8, 128, 512, 2048),
+    "runs_1024_group16": ((1023, 1024, 1025, 3073, 30000) + (17,) * 11, 64, 4, 128, 512, 1024),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("name", SPLITS)
+def test_edges_of_the_longest_partitions_and_runs(name, dtype, cuda_device):
+    """The two-launch form as large batches take it: contexts at the ends of partitions of 512
+    tokens and of second-pass runs."""
+    ctx, H, Hk, D, part, run = SPLITS[name]
+    b = _batch(cuda_device, ctx, H, Hk, D, dtype, 970 + len(name))
+    rows, cap = len(ctx) * Hk, b.block_tables.shape[1] * 16
+    assert _split_form(rows, cap, H // Hk) == (part, run) and cap > 512
+    assert rows < 6 * 148 or cap <= 1536          # (else a CTA takes a context)
+    poison_past_context(b)
+    weights = torch.rand((len(ctx), Hk, max(ctx) + 3), device=cuda_device)
+    before = weights.clone()
+    out = _call(b, weights)
+    torch.cuda.synchronize()
+    pa_check_error()
+    _check(b, before, weights, out, 1, b.cfg.scale)

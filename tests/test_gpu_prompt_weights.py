@@ -258,3 +258,19 @@ def test_weights_beyond_the_largest_number_are_infinite(down, cuda_device):
             assert ((got - want).abs()[fits] <= lim[fits]).all()
             seen += int((want > top + lim).sum())
     assert (seen > 0) == (down > 80)
+
+
+@pytest.mark.parametrize("at,value,left_out", [(3, 171, 2), (0, -1, 0), (0, 41, 0)])
+def test_bad_bounds_alone_are_reported_and_left_out(at, value, left_out, cuda_device):
+    """Every sequence fits the columns: only the bounds are wrong."""
+    p = Prompt(cuda_device, (40, 70, 60), 4, 2, 64, "f16", 81)
+    lse, scale = _lse(p)
+    weights = torch.full((3, 2, 80), 7.0, device=cuda_device)
+    right = int(p.starts[at])
+    p.starts[at] = value
+    pa_prompt_weights(weights, p.q, p.k, lse, p.starts, scale, 8)
+    with pytest.raises(PagedAttentionError, match=f"query, index {left_out}"):
+        pa_check_error()
+    assert (weights[left_out] == 7).all()
+    p.starts[at] = right
+    _check(p, weights, lse, 8, seqs=[s for s in range(3) if s != left_out])
