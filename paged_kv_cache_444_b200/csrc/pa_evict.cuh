@@ -113,6 +113,27 @@ __device__ __forceinline__ void add_cluster_u32(uint32_t addr, uint32_t v) {
                : "memory");
 }
 
+// Loads of what the kernel before may have written while this one had started
+// already (a read-only load must not be used on it), and this one does not write:
+// the compiler may move them over other accesses, but not before the pointer, which
+// after_wait() makes once the other kernel's writes are there.
+template <class T>
+__device__ __forceinline__ const T* after_wait(const T* p) {
+  const T* q;
+  asm volatile("mov.u64 %0, %1;" : "=l"(q) : "l"(p));
+  return q;
+}
+__device__ __forceinline__ float ld_plain(const float* p) {
+  float v;
+  asm("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_plain(const int32_t* p) {
+  int v;
+  asm("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 template <int kThreadsN, int kHeld>
 __global__ void __launch_bounds__(kThreadsN, kHeld > 18 ? 1 : 1024 / kThreadsN)
     evict_select_kernel(const EvictArgs a, int max_run, int list_shift) {
@@ -159,8 +180,8 @@ __global__ void __launch_bounds__(kThreadsN, kHeld > 18 ? 1 : 1024 / kThreadsN)
   const int words = (run + 31) / 32, wper = (words + kWarpsN - 1) / kWarpsN;
   const int w0 = min(warp * wper, words), w1 = min(w0 + wper, words);
   const size_t base = static_cast<size_t>(row) * a.max_tokens + lo;
-  const float* __restrict__ w = a.weights + base;
-  const int32_t* __restrict__ pos = a.positions + base;
+  const float* w = after_wait(a.weights + base);
+  const int32_t* pos = after_wait(a.positions + base);
   const int recorded = min(max(a.recorded_lens[s], 0), n) - lo;   // relative to the run, too
   // recorded positions are held below `sink` and from `first_recent` on; the
   // slots after them, whose positions follow their order, below `held_lo` and
@@ -179,7 +200,7 @@ __global__ void __launch_bounds__(kThreadsN, kHeld > 18 ? 1 : 1024 / kThreadsN)
     if (q + kBatch <= w1 && q * 32 >= recorded && q * 32 >= held_lo &&
         (q + kBatch) * 32 <= held_hi) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) x[u] = __ldg(w + i0 + 32 * u);
+      for (int u = 0; u < kBatch; ++u) x[u] = ld_plain(w + i0 + 32 * u);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) k[u] = claim_key(x[u]);
       return true;
@@ -189,8 +210,8 @@ __global__ void __launch_bounds__(kThreadsN, kHeld > 18 ? 1 : 1024 / kThreadsN)
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + 32 * u;
       const bool in = q + u < w1 && i < run;
-      x[u] = in ? __ldg(w + i) : 0.f;
-      p[u] = in && i < recorded ? __ldg(pos + i) : 0;
+      x[u] = in ? ld_plain(w + i) : 0.f;
+      p[u] = in && i < recorded ? ld_plain(pos + i) : 0;
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -217,8 +238,8 @@ __global__ void __launch_bounds__(kThreadsN, kHeld > 18 ? 1 : 1024 / kThreadsN)
       int p[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        x[u] = 32 * (i + u) < mine ? __ldg(w + i0 + 32 * (i + u)) : 0.f;
-        p[u] = 32 * (i + u) < noted ? __ldg(pos + i0 + 32 * (i + u)) : at + 32 * (i + u);
+        x[u] = 32 * (i + u) < mine ? ld_plain(w + i0 + 32 * (i + u)) : 0.f;
+        p[u] = 32 * (i + u) < noted ? ld_plain(pos + i0 + 32 * (i + u)) : at + 32 * (i + u);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
@@ -620,7 +641,7 @@ __global__ void __launch_bounds__(kCompactThreads)
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     const int i = i0 + u * kCompactThreads;
-    from[u] = i < kept ? __ldg(source + i) : i;
+    from[u] = i < kept ? source[i] : i;
   }
   __syncthreads();                                // the count is clear
 #pragma unroll
