@@ -1276,11 +1276,12 @@ extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const f
   }
   // short runs: keys in registers, with room for a budget of 1024, 4096 or 8192
   // and the tokens since the last eviction.  While all CTAs are resident, twice
-  // the threads for half the words each (8 x 8 rows of 2065 slots: 12.3 -> 10.3 us;
-  // 128 x 8 rows of 4113 took 59 us against 31; as the kernel is now, 6.5 and 19.4)
+  // the threads for half the words each (30 x 8 rows of 4000 slots 11.7 -> 10.5 us,
+  // of 1300 9.5 -> 9.1; 8 x 8 rows of 2065 lose, 6.1 and 6.5; not resident, 128 x 8
+  // rows of 4113 would take 28.1 instead of 19.5).
   // Of many rows each takes a single warp, if that holds its keys (106 x 32 rows of
-  // 349 slots: 20.5 -> 13.7 us, 400 of 276: 8.1 -> 5.6; but two warps with 18
-  // words for 128 x 8 rows of 1017: 14.9 against 12.1)
+  // up to 349 slots 15.4 -> 9.1 us, 400 of 276 6.6 -> 5.6; but two warps with 18
+  // words for 128 x 8 rows of 1017: 10.9 against 9.3).
   if (run <= 32 * 9 && rows > sms)
     return launch_select<32, 9>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 32 * 18 && rows > sms)
@@ -1290,8 +1291,8 @@ extern "C" pa_status pa_evict_select(int32_t* source, int32_t* new_lens, const f
     return launch_select<512, 9>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 256 * 18) return launch_select<256, 18>(a, rows, c, run, shift, as_stream(stream));
   if (run <= 512 * 18) return launch_select<512, 18>(a, rows, c, run, shift, as_stream(stream));
-  // few long rows have an SM a CTA (one of 131072 slots: 16.4 us; streamed, 22.1;
-  // but 16 of 110000, whose clusters are not all resident at once so: 29.5 and 22.5)
+  // few long rows have an SM a CTA (one of 131072 slots: 16.4 us; streamed, 19.2;
+  // but 16 of 110000, whose clusters are not all resident at once so: 30.1 and 22.2)
   if (run <= 512 * 32 && rows * c * 2 <= sms)
     return launch_select<512, 32>(a, rows, c, run, shift, as_stream(stream));
   return launch_select<512, 0>(a, rows, c, run, shift, as_stream(stream));
@@ -1340,8 +1341,8 @@ extern "C" pa_status pa_evict_compact(void* key_cache, void* value_cache, float*
   a.max_blocks_per_seq = static_cast<int>(max_blocks_per_seq);
   a.row_units = static_cast<int>(head_dim * elem_bytes / 16);
   // four slots a thread once a slot a thread would fill the device many times
-  // over (128 x 8 rows of 1000 slots, 17 moves each: 18.8 -> 11.0 us; for 8 x 8
-  // rows of 4096 slots, nearly all moved, it leaves too few CTAs)
+  // over (128 x 8 rows of 1000 slots, 17 moves each: 14.8 -> 8.5 us; for 8 x 8
+  // rows of 4096 slots, nearly all moved, it leaves too few CTAs: 55.5 against 48.2)
   const int64_t rows = num_seqs * num_kv_heads;
   const int64_t slots = budget < max_tokens ? budget : max_tokens;
   const bool many = rows * ((slots + kCompactThreads - 1) / kCompactThreads) > kCompactManyCtas;
@@ -1394,8 +1395,8 @@ WeightsLayout weights_layout(int64_t S, int64_t H, int64_t D, int64_t MB, int64_
 // One CTA a whole context (and no second launch) when a context is one partition
 // anyway, or when there are CTAs for two waves and contexts long enough for the
 // CTA's own last step to be small beside its pages.  128 x 8 contexts of 512 to
-// 4096 tokens: 207.6 us split, 198 single; 130 x 8 of 100 to 30000: 1338, 1297; but
-// 200 x 8 of up to 1000: 82, 90, and 112 x 8 of 4096 each (2.02 waves): 321, 333.
+// 4096 tokens: 205 us split, 195 single; 130 x 8 of 100 to 30000: 1361, 1296; but
+// 200 x 8 of up to 1000: 81, 87, and 112 x 8 of 4096 each (2.02 waves): 318, 340.
 constexpr int kWeightsSingle = 6;        // contexts an SM, at least (three CTAs are resident)
 constexpr int kWeightsSingleParts = 4;   // partitions of the longest context, at least
 
@@ -1667,8 +1668,8 @@ pa_status launch_prompt_weights_t(const CUtensorMap& qm, const CUtensorMap& km,
   // and every CTA of it has a query tile; and, with many tiles (long items, whose
   // lengths differ), while they would not fill them four times.  Eight CTAs only
   // for very few items: clusters that large leave SMs out.  4096 tokens, 32/8 heads:
-  // 176 us without, 108 with four, 133 with eight; 1000 tokens: 49 and 25; but 900 +
-  // 77 + 400 tokens of 32 heads, 256 items: 20 and, with two, 25.
+  // 175 us without, 91 with two, 104 with four, 130 with eight; 1000 tokens: 48, 30, 21
+  // and 24; but 900 + 77 + 400 tokens of 32 heads, 256 items: 18.6 and, with two, 23.9.
   const int tiles = (a.window + a.tile_tokens - 1) / a.tile_tokens;
   PromptWeightsArgs args = a;
   args.cluster = 1;

@@ -62,12 +62,12 @@ __device__ __forceinline__ long long slot_position(const int32_t* positions, int
 // shared memory, where the holes fetch theirs.
 //
 // What bounds it is instructions and the barriers between the steps, not bytes
-// (4 a slot).  8 x 8 rows of 32768 to 131072 slots: 32 us; 105 us when every key
+// (4 a slot).  8 x 8 rows of 32768 to 131072 slots: 30 to 32 us; 105 us when every key
 // was built again for each digit and ranked a slot at a time (315 instructions
 // a word).  128 x 8 rows of 1017 slots: 9.2 us; 31 us with 512 threads and three
 // digits of 11 bits, 12.1 us with each word's bounds looked at in every pass.  One
 // row of 131072 slots, eight CTAs with their keys in registers: 16.4 us; streamed,
-// 22 us, in cycles about a tenth each for the top digit and its exchange, a fifth
+// 19 us, in cycles about a tenth each for the top digit and its exchange, a fifth
 // for flags and lists, the rest shared between the other digits and the ranks and
 // list.
 // ---------------------------------------------------------------------------
@@ -586,8 +586,8 @@ __global__ void __launch_bounds__(kThreadsN, kHeld > 18 ? 1 : 1024 / kThreadsN)
 //
 // A moved token costs 8 D + 16 bytes (read and written), in rows of 2 D bytes at
 // scattered places: 8 x 8 rows of 32768 to 131072 slots cut to 4096, D = 128, about
-// all of them moved: 51 to 54 us for 263 MB, 75 to 79 % of the copy rate.  128 x 8
-// rows of 1017 slots cut to 1000 move 17 rows each: 10.7 us, a chain of dependent
+// all of them moved: 48 us for 263 MB, 84 % of the copy rate.  128 x 8
+// rows of 1017 slots cut to 1000 move 17 rows each: 8.5 us, a chain of dependent
 // loads (source, table, row) rather than bytes.
 // ---------------------------------------------------------------------------
 constexpr int kCompactThreads = 256;

@@ -23,12 +23,13 @@
 // sums, 16 issues the MMAs, 17 the loads, 18 brings each tile's lse into shared
 // memory (negated, in log2 units).
 //
-// Measured: prompts of 4096 and 1333 tokens, 32 heads of 128, whole: 115 us, 1.7
-// times what the 2^x alone take on the special-function unit; issue slots 55 % used,
-// special-function unit 47 %, tensor pipe 35 %.  Instead of the even/odd split, four
-// key blocks an item with a warpgroup each take 124 us, one block's columns over four
-// warpgroups 130.  One prompt of 4096 tokens, 32 heads over 8 (128 items): 109 us with
-// clusters, 176 without; of 1000 tokens 25 and 49.
+// Measured: prompts of 4096 and 1333 tokens, 32 heads of 128, whole: 107 us, 2.3
+// times what the products alone take at cuBLAS's rate (46; the 13 of 16 2^x that are
+// left to the special-function unit take 54); that unit is 60 % used, issue slots 50 %,
+// the tensor pipe 35 %.  Instead of the even/odd split, four key blocks an item with a
+// warpgroup each took 124 us where it took 115, one block's columns over four warpgroups
+// 130.  One prompt of 4096 tokens, 32 heads over 8 (128 items): 104 us with clusters of
+// four, 175 without; of 1000 tokens 24 and 48.
 #pragma once
 
 #include "pa_prompt.cuh"
