@@ -378,7 +378,7 @@ pa_status pa_prompt_attention(void *out, float *lse, const void *query, const vo
  *              sequence s and KV head kv, the sum over those query tokens i >= j
  *              and the query heads h of kv of exp(scale * q[i,h].k[j] - lse[i,h])
  * Entries at or behind a sequence's length stay as they are.  Sums are fp32, in a
- * fixed order.  A sequence longer than max_tokens is left out and reported
+ * fixed order (+inf where a term is beyond the largest fp32).  A sequence longer than max_tokens is left out and reported
  * (PA_CHECK_CONTEXT_LEN, index = s), as are bad bounds (PA_CHECK_QUERY).  Other
  * arguments and limits as pa_prompt_attention.
  */

@@ -16,7 +16,7 @@ from ._lib import (DecodePlan, HostStep, PagedAttentionError, load, pa_check_err
                    pa_decode_fp8, pa_decode_noalloc, pa_decode_shared_prefix, pa_decode_split,
                    pa_decode_split_fp8, pa_decode_weights, pa_evict_compact, pa_evict_select,
                    pa_prefill, pa_prompt_attention, pa_prompt_weights, pa_reduce,
-                   pa_reshape_and_cache, pa_reshape_and_cache_fp8, pa_selftest_wait_timeout)
+                   pa_reshape_and_cache, pa_reshape_and_cache_fp8, pa_selftest_wait_timeout, _stream)
 
 __all__ = [
     "PagedAttentionError", "load", "pa_reshape_and_cache", "pa_decode", "pa_decode_split",
@@ -71,8 +71,8 @@ def _pool_of(stream, device):
     current stream's pool may be in use there while the given stream writes it."""
     if stream is None:
         return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        handle = int(stream)        # 0 and 1: the default stream
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)    # 0 and 1: the default stream
         stream = (torch.cuda.ExternalStream(handle, device) if handle > 1
                   else torch.cuda.default_stream(device))
     return torch.cuda.stream(stream)

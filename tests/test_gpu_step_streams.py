@@ -23,11 +23,18 @@ def _prompt(dev):
                 seq_starts=starts, scale=0.125)
 
 
+class _Wrapped:
+    """Another library's stream: all that is known of it is its handle."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
 def _handles(stream):
-    return {"torch": stream, "handle": stream.cuda_stream}
+    return {"torch": stream, "handle": stream.cuda_stream, "wrapped": _Wrapped(stream)}
 
 
-@pytest.mark.parametrize("kind", ["torch", "handle"])
+@pytest.mark.parametrize("kind", ["torch", "handle", "wrapped"])
 def test_prompt_step_owns_what_it_allocates(kind, cuda_device, monkeypatch):
     """The log-sum-exp lives until the given stream has read it, and the output is
     nothing that the current stream still uses."""
@@ -77,7 +84,7 @@ def test_prompt_step_on_the_default_stream_by_handle(cuda_device):
     pa.pa_check_error()
 
 
-@pytest.mark.parametrize("kind", ["torch", "handle"])
+@pytest.mark.parametrize("kind", ["torch", "handle", "wrapped"])
 def test_decode_step_owns_what_it_allocates(kind, cuda_device, monkeypatch):
     """The same for decode_step: its output, and the workspace of the split form."""
     cfg = workloads.CONFIGS["tiny"]
