@@ -483,6 +483,16 @@ pa_status pa_evict_compact(void *key_cache, void *value_cache, float *weights,
                            void *stream);
 
 /*
+ * pa_evict_commit -- the lengths after an eviction: context_lens[s] and
+ * recorded_lens[s] become new_lens[s], as pa_evict_select wrote it, but stay where
+ * the context length was one it could not use (new_lens[s] = 0 for a context_lens[s]
+ * that is not 0), so that such a sequence is left whole.  The three must not
+ * overlap.
+ */
+pa_status pa_evict_commit(int32_t *context_lens, int32_t *recorded_lens,
+                          const int32_t *new_lens, int64_t num_seqs, void *stream);
+
+/*
  * pa_check_error -- synchronise `stream`, read and clear the current device's
  * error word.  Returns PA_OK if no kernel recorded a problem since the last
  * call, PA_ERR_BOUNDS otherwise (then *detail, if not NULL, receives

@@ -14,7 +14,8 @@ import torch
 
 from ._lib import (DecodePlan, HostStep, PagedAttentionError, load, pa_check_error, pa_copy_blocks, pa_decode,
                    pa_decode_fp8, pa_decode_noalloc, pa_decode_shared_prefix, pa_decode_split,
-                   pa_decode_split_fp8, pa_decode_weights, pa_evict_compact, pa_evict_select,
+                   pa_decode_split_fp8, pa_decode_weights, pa_evict_commit, pa_evict_compact,
+                   pa_evict_select,
                    pa_prefill, pa_prompt_attention, pa_prompt_weights, pa_reduce,
                    pa_reshape_and_cache, pa_reshape_and_cache_fp8, pa_selftest_wait_timeout, _stream)
 
@@ -23,7 +24,7 @@ __all__ = [
     "pa_reduce", "pa_check_error", "pa_decode_noalloc", "pa_decode_shared_prefix",
     "pa_copy_blocks", "pa_reshape_and_cache_fp8", "pa_decode_fp8", "pa_decode_split_fp8",
     "pa_prefill", "pa_prompt_attention", "pa_prompt_weights", "pa_decode_weights",
-    "pa_evict_select", "pa_evict_compact", "pa_selftest_wait_timeout", "SplitWorkspace", "WeightsWorkspace",
+    "pa_evict_select", "pa_evict_compact", "pa_evict_commit", "pa_selftest_wait_timeout", "SplitWorkspace", "WeightsWorkspace",
     "EvictionState", "decode_step", "prompt_step", "HostStep", "DecodePlan",
 ]
 
@@ -160,7 +161,6 @@ class EvictionState:
         self.recorded_lens = torch.zeros(num_seqs, **i32)
         self.source = torch.empty(rows + (budget,), **i32)
         self.new_lens = torch.empty(num_seqs, **i32)
-        self._unusable = torch.empty(num_seqs, dtype=torch.bool, device=device)
 
     def evict(self, key_cache, value_cache, block_tables, context_lens, seq_lens) -> None:
         """Evict down to the budget on the current stream: select, move the kept
@@ -176,7 +176,4 @@ class EvictionState:
                         self.recorded_lens, seq_lens, self.sink, self.recent)
         pa_evict_compact(key_cache, value_cache, self.weights, self.positions, self.source,
                          self.new_lens, block_tables, context_lens, self.recorded_lens, seq_lens)
-        # a new length of 0 is that of an empty sequence, or of a length that cannot be
-        torch.eq(self.new_lens, 0, out=self._unusable).logical_and_(context_lens)
-        for lens in (context_lens, self.recorded_lens):
-            torch.where(self._unusable, lens, self.new_lens, out=lens)
+        pa_evict_commit(context_lens, self.recorded_lens, self.new_lens)

@@ -77,6 +77,7 @@ SIGNATURES = {
     "pa_decode_weights": (_i, [_p] * 3 + [_i64] + [_p] * 5 + [_f] + [_i64] * 9 + [_i, _p]),
     "pa_evict_select": (_i, [_p] * 7 + [_i64] * 6 + [_p]),
     "pa_evict_compact": (_i, [_p] * 10 + [_i64] * 9 + [_p]),
+    "pa_evict_commit": (_i, [_p] * 3 + [_i64, _p]),
 }
 
 _lib: ctypes.CDLL | None = None
@@ -580,6 +581,22 @@ def pa_evict_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, weights
                                  block_tables.data_ptr(), ctx, recorded, seq, S, Hk, D, NB, bs,
                                  blocks[1], W, B, key_cache.element_size(), s)
     _check(st, "pa_evict_compact")
+
+
+def pa_evict_commit(context_lens: torch.Tensor, recorded_lens: torch.Tensor,
+                    new_lens: torch.Tensor, stream=None) -> None:
+    """The lengths after an eviction: context_lens and recorded_lens become
+    new_lens, but stay where pa_evict_select could not use the context length."""
+    S = new_lens.numel()
+    all_lens = (context_lens, recorded_lens, new_lens)
+    for t in all_lens:
+        if t.dtype != torch.int32 or t.shape != (S,) or not t.is_contiguous():
+            raise ValueError("context_lens, recorded_lens and new_lens must be [num_seqs] int32")
+    ctx, recorded, new = (t.data_ptr() for t in all_lens)
+    if abs(ctx - recorded) < 4 * S or abs(ctx - new) < 4 * S or abs(recorded - new) < 4 * S:
+        raise ValueError("context_lens, recorded_lens and new_lens must not share storage")
+    s = _stream_on_one_device(stream, *all_lens)
+    _check(load().pa_evict_commit(ctx, recorded, new, S, s), "pa_evict_commit")
 
 
 class DecodePlan:

@@ -1353,6 +1353,21 @@ extern "C" pa_status pa_evict_compact(void* key_cache, void* value_cache, float*
   return launch_ex(many ? evict_compact_kernel<4> : evict_compact_kernel<1>,
                    static_cast<unsigned>(grid), kCompactThreads, 0, as_stream(stream), 1, a);
 }
+
+extern "C" pa_status pa_evict_commit(int32_t* context_lens, int32_t* recorded_lens,
+                                     const int32_t* new_lens, int64_t num_seqs, void* stream) {
+  if (num_seqs < 0 || num_seqs > INT32_MAX) return PA_ERR_SHAPE;
+  if (num_seqs == 0) return PA_OK;
+  const void* all[] = {context_lens, recorded_lens, new_lens};
+  for (const void* p : all)
+    if (!p) return PA_ERR_NULL;
+  for (const void* p : all)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return PA_ERR_ALIGN;
+  return launch_ex(evict_commit_kernel,
+                   static_cast<unsigned>((num_seqs + kCommitThreads - 1) / kCommitThreads),
+                   kCommitThreads, 0, as_stream(stream), 1, context_lens, recorded_lens, new_lens,
+                   static_cast<int>(num_seqs));
+}
 // <<< eviction
 
 // >>> decode that adds up attention weights (pa_decode_weights): host side.

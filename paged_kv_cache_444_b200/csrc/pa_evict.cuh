@@ -703,4 +703,23 @@ __global__ void __launch_bounds__(kCompactThreads)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Commit: a thread a sequence; launch latency alone (128 x 8 rows of 1017 slots,
+// select, compact and this: 15.4 us; with a copy for each of the lengths, 16.5).
+// ---------------------------------------------------------------------------
+constexpr int kCommitThreads = 128;
+
+__global__ void __launch_bounds__(kCommitThreads)
+    evict_commit_kernel(int32_t* context_lens, int32_t* recorded_lens, const int32_t* new_lens,
+                        int num_seqs) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long s = static_cast<long long>(blockIdx.x) * kCommitThreads + threadIdx.x;
+  if (s >= num_seqs) return;
+  const int n = new_lens[s];
+  if (n == 0 && context_lens[s] != 0) return;
+  context_lens[s] = n;
+  recorded_lens[s] = n;
+}
+
 }  // namespace pa

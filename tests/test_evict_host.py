@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from paged_kv_cache_444_b200 import EvictionState, _lib, pa_evict_compact, pa_evict_select
+from paged_kv_cache_444_b200 import (EvictionState, _lib, pa_evict_commit, pa_evict_compact,
+                                     pa_evict_select)
 
 OK, NULL, SHAPE, DTYPE, ALIGN, UNSUP, CUDA, BOUNDS = range(8)
 FAKE = 0x10000
@@ -204,3 +205,29 @@ def test_lengths_side_by_side_are_apart():
     kc = torch.zeros(4, 16, 1, 64, dtype=torch.float16)
     with pytest.raises(ValueError, match="one CUDA device"):
         state.evict(kc, kc.clone(), i32(4, 2), buf[:4], buf[4:8])
+
+
+COMMIT_ORDER = ("ctx", "recorded", "new_lens", "S")
+COMMIT_BASE = dict(ctx=FAKE, recorded=FAKE + 64, new_lens=FAKE + 128, S=4)
+
+
+@host_only
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(S=-1)), (SHAPE, dict(S=1 << 31)), (NULL, dict(ctx=None)),
+    (NULL, dict(recorded=None)), (NULL, dict(new_lens=None)), (ALIGN, dict(ctx=FAKE + 2)),
+    (OK, dict(S=0, ctx=None)), (CUDA, dict()),
+])
+def test_commit_refusals(want, kw):
+    assert _call("pa_evict_commit", COMMIT_ORDER, COMMIT_BASE, **kw) == want
+
+
+def test_commit_binding_refuses_wrong_tensors():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    good = dict(context_lens=i32(3), recorded_lens=i32(3), new_lens=i32(3))
+    buf = i32(8)
+    for bad in (dict(context_lens=i32(4)), dict(recorded_lens=i32(3).long()),
+                dict(new_lens=i32(6)[::2]), dict(new_lens=i32(3, 1)),
+                dict(context_lens=buf[:3], new_lens=buf[2:5]),
+                dict(context_lens=buf[:3], recorded_lens=buf[:3]), {}):      # (host tensors)
+        with pytest.raises(ValueError):
+            pa_evict_commit(**{**good, **bad})

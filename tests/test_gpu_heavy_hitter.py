@@ -9,8 +9,8 @@ import torch
 
 import evict_reference as ref
 from paged_kv_cache_444_b200 import (EvictionState, PagedAttentionError, WeightsWorkspace,
-                                     pa_check_error, pa_decode_weights, pa_reshape_and_cache,
-                                     prompt_step)
+                                     pa_check_error, pa_decode_weights, pa_evict_commit,
+                                     pa_reshape_and_cache, prompt_step)
 from weights_reference import HALF, attend, out_bound
 
 pytestmark = pytest.mark.gpu
@@ -307,3 +307,22 @@ def test_evict_keeps_a_length_it_cannot_use(cuda_device):
     pa_check_error()
     assert np.array_equal(state.source.cpu().numpy(), source)
     assert ctx.tolist() == new.tolist() == state.recorded_lens.tolist()
+
+
+@pytest.mark.parametrize("S", [1, 127, 128, 129, 1000])
+def test_commit_takes_the_new_lengths_that_there_are(S, cuda_device):
+    rng = np.random.default_rng(S)
+    ctx = rng.integers(-3, 50, S).astype(np.int32)
+    recorded = rng.integers(1, 9, S).astype(np.int32)
+    new = np.where((ctx >= 0) & (ctx <= 40), np.minimum(ctx, 16), 0).astype(np.int32)
+    room = [torch.full((S + 2,), -9, dtype=torch.int32, device=cuda_device) for _ in range(2)]
+    for t, x in zip(room, (ctx, recorded)):
+        t[1:-1] = torch.as_tensor(x)
+    given = torch.as_tensor(new, device=cuda_device)
+    pa_evict_commit(room[0][1:-1], room[1][1:-1], given)
+    torch.cuda.synchronize()
+    unusable = (new == 0) & (ctx != 0)
+    for t, x in zip(room, (ctx, recorded)):
+        want = np.concatenate([[-9], np.where(unusable, x, new), [-9]])
+        assert np.array_equal(t.cpu().numpy(), want)
+    assert np.array_equal(given.cpu().numpy(), new)
